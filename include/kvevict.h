@@ -423,6 +423,9 @@ kvevict_status kvevict_attend_prompt(kvevict_ctx* ctx, const void* q, const void
  *          next (zero it again after KVEVICT_E_TIMEOUT).  Calls on one cache
  *          must not overlap on the GPU (also as captured graphs); caches with
  *          scratch of their own may.
+ * The struct carries no sizes: contexts that use one cache must agree in
+ * batch, num_kv_heads and head_dim (kvevict_kv4_attend: also in the scratch,
+ * whose bytes grow with the group).
  * A row is held in groups of 32 elements: a scale, bf16(largest magnitude /
  * 7), and a code per element, round-to-nearest-even(x / scale) in -7..7; the
  * group's values are code * scale.  A group whose scale would reach 2^63 or

@@ -157,14 +157,23 @@ def _dense(t, shape, dtype, device, what):
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (what, dtype, tuple(shape), device))
 
 
+def kv4_geometry(cfg, device):
+    """What a 4-bit cache of this configuration is sized by: lanes, bytes of a
+    page (0: the configuration has no such cache), device."""
+    return cfg.batch * cfg.num_kv_heads, lib().kvevict_kv4_page_bytes(ctypes.byref(cfg)), device
+
+
 class Kv4Cache:
     """Device buffers of one 4-bit cache (kvevict_kv4): pages, the lanes' page
     table and the attention's scratch.  Caches of several layers may share one
-    pool of pages: pass `pages`, and a table per layer."""
+    pool of pages: pass `pages`, and a table per layer.  Other engines of the
+    same lanes, head_dim and device may use the cache (to attend, no larger
+    a group); any other engine's calls refuse it."""
 
     def __init__(self, eng, num_pages, max_pages, table=None, pages=None):
         L, c = lib(), ctypes.byref(eng.cfg)
-        page = L.kvevict_kv4_page_bytes(c)
+        self.geometry = kv4_geometry(eng.cfg, eng.device)
+        page = self.geometry[1]
         if page == 0:
             raise KvevictError(6, "kvevict_kv4_page_bytes")
         self.num_pages, self.max_pages, self.page_bytes = int(num_pages), int(max_pages), page
@@ -177,7 +186,8 @@ class Kv4Cache:
         _dense(pages, (num_pages, page), torch.uint8, eng.device, "pages")
         _dense(table, (eng.lanes, max_pages), torch.int32, eng.device, "table")
         self.pages, self.table = pages, table
-        self.scratch = torch.zeros((L.kvevict_kv4_scratch_bytes(c),), dtype=torch.uint8, device=eng.device)
+        self.scratch_bytes = L.kvevict_kv4_scratch_bytes(c)
+        self.scratch = torch.zeros((self.scratch_bytes,), dtype=torch.uint8, device=eng.device)
         self.c = Kv4(pages.data_ptr(), table.data_ptr(), self.scratch.data_ptr(), self.num_pages, self.max_pages)
         self.ref = ctypes.byref(self.c)
         _check(L.kvevict_kv4_validate(c, self.ref), "kvevict_kv4_validate")
@@ -197,6 +207,8 @@ class Engine:
         self.device = torch.device(device)
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self.kv4_geometry = kv4_geometry(cfg, self.device)
+        self.kv4_scratch_bytes = L.kvevict_kv4_scratch_bytes(ctypes.byref(cfg))
         c = cfg
         lanes = c.batch * c.num_kv_heads
         self.lanes = lanes
@@ -450,6 +462,13 @@ class Engine:
         """A 4-bit cache for this engine's lanes (Kv4Cache)."""
         return Kv4Cache(self, num_pages, max_pages, table=table, pages=pages)
 
+    def _cache_ref(self, cache, scratch=0):
+        # the library sees addresses only: a cache sized for other lanes or rows would be overrun
+        if not (cache.geometry == self.kv4_geometry and cache.scratch_bytes >= scratch):
+            raise ValueError("the cache was made for %s (lanes, page bytes, device) and %d bytes of scratch; this engine needs %s and %d"
+                             % (cache.geometry, cache.scratch_bytes, self.kv4_geometry, scratch))
+        return cache.ref
+
     def _lane_ints(self, t, what):
         if t is not None:
             _dense(t, (self.lanes,), torch.int32, self.device, what)
@@ -457,35 +476,35 @@ class Engine:
 
     def kv4_write(self, cache, starts, k, v, stream=None):
         """kvevict_kv4_write: k, v [B][Hkv][n][d] at indices starts[lane] and after."""
-        c = self.cfg
+        c, ref = self.cfg, self._cache_ref(cache)
         _need(k.dim() == 4, "k must be [batch][Hkv][n][d]")
         n = k.shape[2]
         for t, w in ((k, "k"), (v, "v")):
             _dense(t, (c.batch, c.num_kv_heads, n, c.head_dim), torch.bfloat16, self.device, w)
-        _check(lib().kvevict_kv4_write(self.h, cache.ref, self._lane_ints(starts, "starts"), n,
+        _check(lib().kvevict_kv4_write(self.h, ref, self._lane_ints(starts, "starts"), n,
                                        k.data_ptr(), v.data_ptr(), self._on(stream)), "kvevict_kv4_write")
 
     def kv4_pack(self, layer, cache, stream=None):
         """kvevict_kv4_pack: every kept token of an engine layer, from index 0."""
-        _check(lib().kvevict_kv4_pack(self.h, layer, cache.ref, self._on(stream)), "kvevict_kv4_pack")
+        _check(lib().kvevict_kv4_pack(self.h, layer, self._cache_ref(cache), self._on(stream)), "kvevict_kv4_pack")
 
     def kv4_read(self, cache, starts, n, lens=None, k=None, v=None, stream=None):
         """kvevict_kv4_read: the values of n tokens a lane, [B][Hkv][n][d]."""
-        c = self.cfg
+        c, ref = self.cfg, self._cache_ref(cache)
         shp = (c.batch, c.num_kv_heads, n, c.head_dim)
         # rows past a lane's end are not written
         k = torch.zeros(shp, dtype=torch.bfloat16, device=self.device) if k is None else k
         v = torch.zeros(shp, dtype=torch.bfloat16, device=self.device) if v is None else v
         _dense(k, shp, torch.bfloat16, self.device, "k")
         _dense(v, shp, torch.bfloat16, self.device, "v")
-        _check(lib().kvevict_kv4_read(self.h, cache.ref, self._lane_ints(starts, "starts"),
+        _check(lib().kvevict_kv4_read(self.h, ref, self._lane_ints(starts, "starts"),
                                       self._lane_ints(lens, "lens"), n, k.data_ptr(), v.data_ptr(),
                                       self._on(stream)), "kvevict_kv4_read")
         return k, v
 
     def kv4_attend(self, cache, lens, q, sinks=0, window=0, out=None, lse=None, stream=None):
         """kvevict_kv4_attend: (out [B][Hq][d], lse [B][Hq])."""
-        c, dev = self.cfg, self.device
+        c, dev, ref = self.cfg, self.device, self._cache_ref(cache, self.kv4_scratch_bytes)
         shp = (c.batch, c.num_q_heads, c.head_dim)
         _dense(q, shp, torch.bfloat16, dev, "q")
         if out is None:
@@ -495,7 +514,7 @@ class Engine:
         _dense(out, shp, torch.bfloat16, dev, "out")
         _dense(lse, shp[:2], torch.float32, dev, "lse")
         _need(lens is not None, "lens")
-        _check(lib().kvevict_kv4_attend(self.h, cache.ref, self._lane_ints(lens, "lens"), q.data_ptr(),
+        _check(lib().kvevict_kv4_attend(self.h, ref, self._lane_ints(lens, "lens"), q.data_ptr(),
                                         sinks, window, out.data_ptr(), lse.data_ptr(), self._on(stream)),
                "kvevict_kv4_attend")
         return out, lse

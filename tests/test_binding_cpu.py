@@ -1,0 +1,77 @@
+"""What the Python binding refuses before an address reaches the library.
+Engines and caches here have no device memory: a refused call touches none."""
+import shutil
+import os
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.skipif(not (shutil.which("nvcc") or os.path.exists("/usr/local/cuda/bin/nvcc")),
+                                reason="nvcc not available")
+
+
+@pytest.fixture(scope="module")
+def B():
+    from kv_cache_token_gb300 import build
+    build.build()
+    from kv_cache_token_gb300 import binding
+    return binding
+
+
+def config(B, **kw):
+    f = dict(policy=B.H2O, num_layers=1, batch=2, num_q_heads=8, num_kv_heads=2, head_dim=128, kv_dtype=B.BF16,
+             blocks_per_pool=8, max_tokens=16, budget=8, recent_window=2, obs_window=1, pool_kernel=1)
+    f.update(kw)
+    return B.config_from(**f)
+
+
+def bare_engine(B, **kw):
+    """An engine without buffers: enough for argument checks."""
+    import ctypes
+    e = B.Engine.__new__(B.Engine)
+    e.cfg, e.device, e.h = config(B, **kw), torch.device("cuda", 0), None
+    e.lanes = e.cfg.batch * e.cfg.num_kv_heads
+    e.kv_dtype = torch.bfloat16
+    e.kv4_geometry = B.kv4_geometry(e.cfg, e.device)
+    e.kv4_scratch_bytes = B.lib().kvevict_kv4_scratch_bytes(ctypes.byref(e.cfg))
+    return e
+
+
+def bare_cache(B, eng):
+    c = B.Kv4Cache.__new__(B.Kv4Cache)
+    c.geometry, c.scratch_bytes, c.ref = eng.kv4_geometry, eng.kv4_scratch_bytes, "ref"
+    return c
+
+
+@pytest.mark.parametrize("other", [dict(batch=3), dict(batch=1), dict(num_kv_heads=4), dict(head_dim=64),
+                                   dict(batch=16, num_q_heads=16, num_kv_heads=8)])
+def test_a_cache_of_another_engine_is_refused(B, other):
+    mine, their = bare_engine(B), bare_engine(B, **other)
+    c = bare_cache(B, their)
+    assert their._cache_ref(c, their.kv4_scratch_bytes) == "ref"
+    k = torch.zeros((2, 2, 4, 128), dtype=torch.bfloat16)
+    q, lens = torch.zeros((2, 8, 128), dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    for call in (lambda: mine.kv4_write(c, None, k, k), lambda: mine.kv4_pack(0, c), lambda: mine.kv4_read(c, None, 4, k=k, v=k),
+                 lambda: mine.kv4_attend(c, lens, q)):
+        with pytest.raises(ValueError, match="cache was made for"):
+            call()
+
+
+def test_a_larger_group_may_not_attend_on_a_smaller_scratch(B):
+    small, large = bare_engine(B, num_q_heads=4), bare_engine(B, num_q_heads=16)
+    assert small.kv4_geometry == large.kv4_geometry and small.kv4_scratch_bytes < large.kv4_scratch_bytes
+    c = bare_cache(B, small)
+    q, lens = torch.zeros((2, 16, 128), dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="scratch"):
+        large.kv4_attend(c, lens, q)
+    # storing and reading need no scratch, and a smaller group fits a larger one's
+    assert large._cache_ref(c) == "ref"
+    assert small._cache_ref(bare_cache(B, large), small.kv4_scratch_bytes) == "ref"
+
+
+def test_a_cache_on_another_device_is_refused(B):
+    a, b = bare_engine(B), bare_engine(B)
+    b.device = torch.device("cuda", 1)
+    b.kv4_geometry = B.kv4_geometry(b.cfg, b.device)
+    with pytest.raises(ValueError, match="cache was made for"):
+        a.kv4_pack(0, bare_cache(B, b))
