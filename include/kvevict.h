@@ -367,7 +367,8 @@ kvevict_status kvevict_attend_static(kvevict_ctx* ctx, int layer, const void* q,
  * the status word; only kvevict_kv4_pack reads engine tables, and none changes
  * engine state.  The context's device must be current and the stream one of
  * its streams (KVEVICT_E_INVALID_ARG for another device).  Outputs must not
- * overlap inputs. */
+ * overlap inputs.  int32 and fp32 arrays are 4-byte aligned
+ * (KVEVICT_E_INVALID_ARG otherwise). */
 
 /* Per-head norm and rotation of a projection, written in the layouts of the
  * other calls.  qkv holds one row per token, batch_stride elements from

@@ -500,6 +500,7 @@ static bool on_device(const kvevict_ctx* ctx) {
   return cudaGetDevice(&dev) == cudaSuccess && dev == ctx->c.device;
 }
 static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+static bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }   // int32 and fp32 arrays
 
 kvevict_status kvevict_norm_rope(kvevict_ctx* ctx, const void* qkv, int64_t batch_stride, int64_t row_stride,
                                  int32_t n, const void* wq, const void* wk, float eps, const int32_t* pos,
@@ -510,7 +511,7 @@ kvevict_status kvevict_norm_rope(kvevict_ctx* ctx, const void* qkv, int64_t batc
   const kve::Dims& dm = ctx->c.dims;
   const int64_t per16 = dm.dtype == KVEVICT_BF16 ? 8 : 4;   // elements in 16 bytes
   if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(v_out) || !aligned16(wq) ||
-      !aligned16(wk) || row_stride % per16 != 0 ||
+      !aligned16(wk) || !aligned4(pos) || row_stride % per16 != 0 ||
       row_stride < static_cast<int64_t>(dm.Hq + 2 * dm.Hkv) * dm.d)
     return KVEVICT_E_INVALID_ARG;
   if (dm.B > 1 && (batch_stride < 0 || batch_stride % per16 != 0)) return KVEVICT_E_INVALID_ARG;
@@ -528,7 +529,8 @@ kvevict_status kvevict_attend_prompt(kvevict_ctx* ctx, const void* q, const void
                                      int32_t sinks, int32_t window, void* out, float* lse, void* stream) {
   const CallRange range("kvevict_attend_prompt");
   if (!ctx || !q || !k || !v || !out || n < 1 || sinks < 0 || window < 0) return KVEVICT_E_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return KVEVICT_E_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned4(lse))
+    return KVEVICT_E_INVALID_ARG;
   if (ctx->c.dims.dtype != KVEVICT_BF16) return KVEVICT_E_DTYPE;
   if (!on_device(ctx)) return KVEVICT_E_INVALID_ARG;
   kve::note_other(ctx->c);
@@ -571,7 +573,7 @@ kvevict_status kvevict_kv4_write(kvevict_ctx* ctx, const kvevict_kv4* cache, con
   const CallRange range("kvevict_kv4_write");
   const kvevict_status s = kv4_check(ctx, cache);
   if (s != KVEVICT_OK) return s;
-  if (n < 1 || !k || !v || !aligned16(k) || !aligned16(v)) return KVEVICT_E_INVALID_ARG;
+  if (n < 1 || !k || !v || !aligned16(k) || !aligned16(v) || !aligned4(starts)) return KVEVICT_E_INVALID_ARG;
   kve::note_other(ctx->c);
   return cuda_status(kve::launch_kv4_write(ctx->c, *cache, starts, n, k, v, static_cast<cudaStream_t>(stream)));
 }
@@ -590,7 +592,8 @@ kvevict_status kvevict_kv4_read(kvevict_ctx* ctx, const kvevict_kv4* cache, cons
   const CallRange range("kvevict_kv4_read");
   const kvevict_status s = kv4_check(ctx, cache);
   if (s != KVEVICT_OK) return s;
-  if (n < 1 || !k || !v || !aligned16(k) || !aligned16(v)) return KVEVICT_E_INVALID_ARG;
+  if (n < 1 || !k || !v || !aligned16(k) || !aligned16(v) || !aligned4(starts) || !aligned4(lens))
+    return KVEVICT_E_INVALID_ARG;
   kve::note_other(ctx->c);
   return cuda_status(kve::launch_kv4_read(ctx->c, *cache, starts, lens, n, k, v, static_cast<cudaStream_t>(stream)));
 }
@@ -600,7 +603,8 @@ kvevict_status kvevict_kv4_attend(kvevict_ctx* ctx, const kvevict_kv4* cache, co
   const CallRange range("kvevict_kv4_attend");
   const kvevict_status s = kv4_check(ctx, cache);
   if (s != KVEVICT_OK) return s;
-  if (!lens || !q || !out || !aligned16(q) || !aligned16(out) || sinks < 0 || window < 0)
+  if (!lens || !q || !out || !aligned16(q) || !aligned16(out) || !aligned4(lens) || !aligned4(lse) || sinks < 0 ||
+      window < 0)
     return KVEVICT_E_INVALID_ARG;
   kve::note_other(ctx->c);
   return cuda_status(kve::launch_kv4_attend(ctx->c, *cache, lens, q, sinks, window, out, lse,
