@@ -34,8 +34,8 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(SRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [
-        os.path.abspath(__file__)]
+    headers = [os.path.join(SRC, "*.cuh"), os.path.join(SRC, "*.h"), os.path.join(INCLUDE, "*.h")]
+    return _sources() + [p for h in headers for p in glob.glob(h)] + [os.path.abspath(__file__)]
 
 
 def up_to_date():

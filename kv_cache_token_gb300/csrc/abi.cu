@@ -286,8 +286,6 @@ kvevict_status kvevict_create(const kvevict_config* cfg, const kvevict_buffers* 
   ctx->c.dims = kve::make_dims(*cfg);
   ctx->c.sm_count = sms;
   ctx->c.device = dev;
-  ctx->c.last_layer = -1;
-  ctx->c.last_kind = kve::kLaunchOther;
   for (int c = 0; c < kve::kScratchBufs; ++c) ctx->c.epi_launches[c] = 0u;
   ctx->c.tmaps = nullptr;
   ctx->c.rope_base = 0.0;
@@ -348,6 +346,12 @@ void kvevict_destroy(kvevict_ctx* ctx) {
 
 static kvevict_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVEVICT_OK : KVEVICT_E_CUDA; }
 
+// Kernels without early start (they let no successor start before they complete) were launched, or not.
+static kvevict_status launched(kvevict_ctx* ctx, void* stream, cudaError_t e) {
+  ctx->c.history.other(stream, e == cudaSuccess);
+  return cuda_status(e);
+}
+
 kvevict_status kvevict_set_layer_budget(kvevict_ctx* ctx, int layer, int32_t budget, int32_t recent_window) {
   if (!ctx || layer < 0 || layer >= ctx->c.dims.L || recent_window < 1) return KVEVICT_E_INVALID_ARG;
   if (recent_window >= budget) return KVEVICT_E_RECENT_GE_BUDGET;
@@ -368,18 +372,17 @@ kvevict_status kvevict_relocate(kvevict_ctx* ctx, int layer, int32_t* freed, int
                                 int32_t* n_moves, void* stream) {
   const CallRange range("kvevict_relocate");
   if (!ctx || layer < 0 || layer >= ctx->c.dims.L) return KVEVICT_E_INVALID_ARG;
-  kve::note_other(ctx->c);
-  return cuda_status(kve::launch_compact(ctx->c, ctx->c.ws_reloc, layer, ctx->c.no_victims, ctx->c.no_victims, true,
-                                         freed, n_freed, moves, n_moves, static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_compact(ctx->c, ctx->c.ws_reloc, layer, ctx->c.no_victims,
+                                                   ctx->c.no_victims, true, freed, n_freed, moves, n_moves,
+                                                   static_cast<cudaStream_t>(stream)));
 }
 
 kvevict_status kvevict_reset(kvevict_ctx* ctx, void* stream) {
   if (!ctx) return KVEVICT_E_INVALID_ARG;
-  kve::note_other(ctx->c);
   for (int l = 0; l < ctx->c.dims.L; ++l) ctx->c.layer_steady[l] = true;   // every lane empty
   // the reset zeroes the epilogue counts of the scratch copies
   for (int c = 0; c < kve::kScratchBufs; ++c) ctx->c.epi_launches[c] = 0u;
-  return cuda_status(kve::launch_reset(ctx->c, static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_reset(ctx->c, static_cast<cudaStream_t>(stream)));
 }
 
 kvevict_status kvevict_prefill(kvevict_ctx* ctx, int layer, const void* k_ctx, const void* v_ctx, int32_t n,
@@ -387,9 +390,8 @@ kvevict_status kvevict_prefill(kvevict_ctx* ctx, int layer, const void* k_ctx, c
   const CallRange range("kvevict_prefill");
   if (!ctx || !k_ctx || !v_ctx || layer < 0 || layer >= ctx->c.dims.L || n < 1 || n > ctx->c.dims.cap - 1)
     return KVEVICT_E_INVALID_ARG;
-  kve::note_other(ctx->c);
   ctx->c.layer_steady[layer] = ctx->c.layer_steady[layer] && n <= ctx->c.layer_budget[layer];
-  return cuda_status(kve::launch_prefill(ctx->c, layer, k_ctx, v_ctx, n, static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_prefill(ctx->c, layer, k_ctx, v_ctx, n, static_cast<cudaStream_t>(stream)));
 }
 
 kvevict_status kvevict_decode_step(kvevict_ctx* ctx, int layer, const void* q, const void* k_new, const void* v_new,
@@ -412,7 +414,7 @@ kvevict_status kvevict_attend(kvevict_ctx* ctx, int layer, const void* q, const 
   if (ctx->c.dims.policy == KVEVICT_DROPKV && !kve::has_ring(ctx->c.cfg)) return KVEVICT_E_INVALID_ARG;
   if (!q) return KVEVICT_OK;
   const cudaError_t e = kve::launch_attend(ctx->c, layer, q, k_new, v_new, static_cast<cudaStream_t>(stream), false);
-  if (e == cudaSuccess) kve::note_attend(ctx->c, layer);
+  if (e == cudaSuccess) ctx->c.history.attend(layer, stream);
   return cuda_status(e);
 }
 
@@ -429,12 +431,12 @@ kvevict_status kvevict_finish_step(kvevict_ctx* ctx, int layer, const void* q, c
   cudaError_t e = kve::launch_epilogue(ctx->c, layer, q != nullptr, new_pos, k_new, v_new, out, lse, victims,
                                        n_victims, st, &apply_kernel);
   if (e == cudaSuccess) {
-    kve::note_epilogue(ctx->c, layer);
+    kve::note_epilogue(ctx->c, layer, st);
     ctx->c.layer_steady[layer] = true;
   }
   if (e == cudaSuccess && apply_kernel) {
     e = kve::launch_allocate_apply(ctx->c, layer, k_new, v_new, false, nullptr, st, false);
-    kve::note_apply(ctx->c);
+    ctx->c.history.apply(stream);
   }
   return cuda_status(e);
 }
@@ -448,9 +450,8 @@ kvevict_status kvevict_score(kvevict_ctx* ctx, int layer, const void* q_win, int
   if (reinterpret_cast<uintptr_t>(q_win) % 16 || reinterpret_cast<uintptr_t>(a_out) % 16)
     return KVEVICT_E_INVALID_ARG;   // 16-byte row copies and stores
   if (ctx->c.dims.dtype != KVEVICT_BF16 || ctx->c.dims.d != 128) return KVEVICT_E_DTYPE;
-  kve::note_other(ctx->c);
-  return cuda_status(kve::launch_score(ctx->c, layer, q_win, w, q_pos, lse, a_out, scores,
-                                       static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_score(ctx->c, layer, q_win, w, q_pos, lse, a_out, scores,
+                                                 static_cast<cudaStream_t>(stream)));
 }
 
 kvevict_status kvevict_score_mass(kvevict_ctx* ctx, int layer, const void* q_win, int32_t w, const int32_t* q_pos,
@@ -465,9 +466,8 @@ kvevict_status kvevict_score_mass(kvevict_ctx* ctx, int layer, const void* q_win
   const int pk = ctx->c.cfg.pool_kernel;
   if (kind == KVEVICT_MASS_SNAPKV && (pk < 1 || pk % 2 == 0)) return KVEVICT_E_POOL_KERNEL_EVEN;
   const int pool_r = kind == KVEVICT_MASS_SNAPKV && pk > 1 ? (pk - 1) / 2 : -1;
-  kve::note_other(ctx->c);
-  return cuda_status(kve::launch_score_mass(ctx->c, layer, q_win, w, q_pos, kind == KVEVICT_MASS_H2O, pool_r, lse,
-                                            scores, static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_score_mass(ctx->c, layer, q_win, w, q_pos, kind == KVEVICT_MASS_H2O, pool_r,
+                                                      lse, scores, static_cast<cudaStream_t>(stream)));
 }
 
 kvevict_status kvevict_select(kvevict_ctx* ctx, const void* keys, int32_t key_dtype, const int32_t* positions,
@@ -479,19 +479,17 @@ kvevict_status kvevict_select(kvevict_ctx* ctx, const void* keys, int32_t key_dt
     return KVEVICT_E_INVALID_ARG;
   if (key_dtype != KVEVICT_KEY_F32 && key_dtype != KVEVICT_KEY_F64) return KVEVICT_E_DTYPE;
   if (n_lanes == 0) return KVEVICT_OK;
-  kve::note_other(ctx->c);
-  return cuda_status(kve::launch_select(ctx->c, keys, key_dtype, positions, counts, n_lanes, stride, budget,
-                                        recent_window, victims, n_victims, static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_select(ctx->c, keys, key_dtype, positions, counts, n_lanes, stride, budget,
+                                                  recent_window, victims, n_victims,
+                                                  static_cast<cudaStream_t>(stream)));
 }
 
 kvevict_status kvevict_compact(kvevict_ctx* ctx, int layer, const int32_t* victims, const int32_t* n_victims,
                                int32_t* freed, int32_t* n_freed, int32_t* moves, int32_t* n_moves, void* stream) {
   const CallRange range("kvevict_compact");
   if (!ctx || layer < 0 || layer >= ctx->c.dims.L || !victims || !n_victims) return KVEVICT_E_INVALID_ARG;
-  kve::note_other(ctx->c);
-  return cuda_status(kve::launch_compact(ctx->c, ctx->c.ws, layer, victims, n_victims, false, freed, n_freed, moves,
-                                         n_moves,
-                                         static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_compact(ctx->c, ctx->c.ws, layer, victims, n_victims, false, freed, n_freed,
+                                                   moves, n_moves, static_cast<cudaStream_t>(stream)));
 }
 
 // The calls around the eviction launch on the context's device only.
@@ -519,7 +517,7 @@ kvevict_status kvevict_norm_rope(kvevict_ctx* ctx, const void* qkv, int64_t batc
       !(eps >= 0.f) || !(eps <= 1e30f))
     return KVEVICT_E_INVALID_ARG;
   if (!on_device(ctx)) return KVEVICT_E_INVALID_ARG;
-  kve::note_inputs(ctx->c);
+  ctx->c.history.inputs(stream);
   return cuda_status(kve::launch_norm_rope(ctx->c, qkv, dm.B > 1 ? batch_stride : 0, row_stride, n, wq, wk, eps, pos,
                                            pos0, rotary_dim, base, interleaved, q_out, k_out, v_out,
                                            static_cast<cudaStream_t>(stream)));
@@ -533,9 +531,8 @@ kvevict_status kvevict_attend_prompt(kvevict_ctx* ctx, const void* q, const void
     return KVEVICT_E_INVALID_ARG;
   if (ctx->c.dims.dtype != KVEVICT_BF16) return KVEVICT_E_DTYPE;
   if (!on_device(ctx)) return KVEVICT_E_INVALID_ARG;
-  kve::note_other(ctx->c);
-  return cuda_status(kve::launch_attend_prompt(ctx->c, q, k, v, n, sinks, window, out, lse,
-                                               static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_attend_prompt(ctx->c, q, k, v, n, sinks, window, out, lse,
+                                                         static_cast<cudaStream_t>(stream)));
 }
 
 size_t kvevict_kv4_page_bytes(const kvevict_config* c) {
@@ -574,8 +571,8 @@ kvevict_status kvevict_kv4_write(kvevict_ctx* ctx, const kvevict_kv4* cache, con
   const kvevict_status s = kv4_check(ctx, cache);
   if (s != KVEVICT_OK) return s;
   if (n < 1 || !k || !v || !aligned16(k) || !aligned16(v) || !aligned4(starts)) return KVEVICT_E_INVALID_ARG;
-  kve::note_other(ctx->c);
-  return cuda_status(kve::launch_kv4_write(ctx->c, *cache, starts, n, k, v, static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_kv4_write(ctx->c, *cache, starts, n, k, v,
+                                                     static_cast<cudaStream_t>(stream)));
 }
 
 kvevict_status kvevict_kv4_pack(kvevict_ctx* ctx, int layer, const kvevict_kv4* cache, void* stream) {
@@ -583,8 +580,7 @@ kvevict_status kvevict_kv4_pack(kvevict_ctx* ctx, int layer, const kvevict_kv4* 
   const kvevict_status s = kv4_check(ctx, cache);
   if (s != KVEVICT_OK) return s;
   if (layer < 0 || layer >= ctx->c.dims.L) return KVEVICT_E_INVALID_ARG;
-  kve::note_other(ctx->c);
-  return cuda_status(kve::launch_kv4_pack(ctx->c, layer, *cache, static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_kv4_pack(ctx->c, layer, *cache, static_cast<cudaStream_t>(stream)));
 }
 
 kvevict_status kvevict_kv4_read(kvevict_ctx* ctx, const kvevict_kv4* cache, const int32_t* starts,
@@ -594,8 +590,8 @@ kvevict_status kvevict_kv4_read(kvevict_ctx* ctx, const kvevict_kv4* cache, cons
   if (s != KVEVICT_OK) return s;
   if (n < 1 || !k || !v || !aligned16(k) || !aligned16(v) || !aligned4(starts) || !aligned4(lens))
     return KVEVICT_E_INVALID_ARG;
-  kve::note_other(ctx->c);
-  return cuda_status(kve::launch_kv4_read(ctx->c, *cache, starts, lens, n, k, v, static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_kv4_read(ctx->c, *cache, starts, lens, n, k, v,
+                                                    static_cast<cudaStream_t>(stream)));
 }
 
 kvevict_status kvevict_kv4_attend(kvevict_ctx* ctx, const kvevict_kv4* cache, const int32_t* lens, const void* q,
@@ -606,16 +602,14 @@ kvevict_status kvevict_kv4_attend(kvevict_ctx* ctx, const kvevict_kv4* cache, co
   if (!lens || !q || !out || !aligned16(q) || !aligned16(out) || !aligned4(lens) || !aligned4(lse) || sinks < 0 ||
       window < 0)
     return KVEVICT_E_INVALID_ARG;
-  kve::note_other(ctx->c);
-  return cuda_status(kve::launch_kv4_attend(ctx->c, *cache, lens, q, sinks, window, out, lse,
-                                            static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_kv4_attend(ctx->c, *cache, lens, q, sinks, window, out, lse,
+                                                      static_cast<cudaStream_t>(stream)));
 }
 
 kvevict_status kvevict_stats(kvevict_ctx* ctx, int layer, int64_t* out, void* stream) {
   if (!ctx || !out || layer < 0 || layer >= ctx->c.dims.L) return KVEVICT_E_INVALID_ARG;
-  kve::note_other(ctx->c);
-  return cuda_status(kve::launch_stats(ctx->c, layer, reinterpret_cast<long long*>(out),
-                                       static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_stats(ctx->c, layer, reinterpret_cast<long long*>(out),
+                                                 static_cast<cudaStream_t>(stream)));
 }
 
 int32_t kvevict_kernels_per_decode_step(const kvevict_ctx* ctx) {
@@ -625,8 +619,7 @@ int32_t kvevict_kernels_per_decode_step(const kvevict_ctx* ctx) {
 
 kvevict_status kvevict_check_wait_timeout(kvevict_ctx* ctx, int32_t polls, void* stream) {
   if (!ctx || polls < 1 || polls > (1 << 22)) return KVEVICT_E_INVALID_ARG;
-  kve::note_other(ctx->c);
-  return cuda_status(kve::launch_wait_check(ctx->c, polls, static_cast<cudaStream_t>(stream)));
+  return launched(ctx, stream, kve::launch_wait_check(ctx->c, polls, static_cast<cudaStream_t>(stream)));
 }
 
 kvevict_status kvevict_last_error(kvevict_ctx* ctx, char* buf, size_t len) {

@@ -786,8 +786,8 @@ cudaError_t launch_attend(const Ctx& ctx, int layer, const void* q, const void* 
   a.P = dm.P;
   a.scale2 = 1.4426950408889634f / sqrtf(static_cast<float>(dm.d));
   a.early_trigger = early_trigger ? 1 : 0;
-  // early start: see attend_early_ok (the kernel guards itself)
-  const bool pdl = attend_early_ok(ctx);
+  // early start: see launch_history.h (the kernel guards itself)
+  const bool pdl = ctx.history.attend_early(stream);
   if (dm.dtype == KVEVICT_BF16) {
     if (dm.lanes > kMaxLanesSmem) return cudaErrorInvalidValue;
     const int grid = ctx.sm_count * ctx.attend_ctas_per_sm;

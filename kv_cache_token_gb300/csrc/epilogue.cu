@@ -2481,7 +2481,7 @@ cudaError_t launch_epilogue(const Ctx& ctx, int layer, bool has_q, int new_pos, 
   // layer's attention launch: the epilogue then reads, before its dependency
   // wait, tables no running kernel writes.  A query-less epilogue waits for
   // its predecessor.
-  const bool pdl = has_q && ctx.last_kind == kLaunchAttend && ctx.last_layer == layer;
+  const bool pdl = has_q && ctx.history.epilogue_early(layer);
   const bool ring = ctx.dims.policy != KVEVICT_H2O;
   const dim3 grid(ctx.dims.lanes);
   // the lean H2O epilogue when every lane is within its budget (a hint from

@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 
 #include "../../include/kvevict.h"
+#include "launch_history.h"
 
 namespace kve {
 
@@ -113,12 +114,10 @@ struct Ctx {
   // One CTA of the lean H2O epilogue fits on an SM beside attend_ctas_per_sm
   // CTAs of the attention kernel (registers, shared memory, threads).
   bool lean_coresident;
-  // Launch history for programmatic dependent launch: the most recent launch
-  // (kLaunch*, its layer), and per scratch copy the number of decode
-  // epilogues launched on it (wrapping), whose CTAs the next attention on
-  // that copy waits for (Workspace::reads_done).
-  int last_layer;
-  int last_kind;
+  // Launch history for programmatic dependent launch, and per scratch copy the
+  // number of decode epilogues launched on it (wrapping), whose CTAs the next
+  // attention on that copy waits for (Workspace::reads_done).
+  LaunchHistory history;
   uint32_t epi_launches[kScratchBufs];
   // TMA tensor maps over each layer's K and V pool ([P * 16 rows][d], bf16,
   // 128-byte swizzle, boxes of one 64-element half row x 1, 16 or 64 rows),
@@ -159,31 +158,10 @@ struct Ctx {
   uint64_t rope_freq[kRopePairs];
 };
 
-enum : int { kLaunchOther = 0, kLaunchAttend = 1, kLaunchEpilogue = 2, kLaunchApply = 3, kLaunchInputs = 4 };
-
-// Launch-history rules (host).  An attention kernel checks on the device,
-// before it writes anything, that every decode epilogue launched earlier on
-// its scratch copy has finished (which also covers every earlier epilogue of
-// its own layer, which uses the same copy), so it may start early after any
-// kernel but a separate apply kernel, which rewrites a layer's tables after
-// its epilogue has finished, and one that writes a step's queries, keys and
-// values, which the attention reads at once.  The epilogue starts early only
-// right after its layer's attention launch.
-inline bool attend_early_ok(const Ctx& c) { return c.last_kind != kLaunchApply && c.last_kind != kLaunchInputs; }
-inline void note_attend(Ctx& c, int layer) {
-  c.last_kind = kLaunchAttend;
-  c.last_layer = layer;
-}
-inline void note_epilogue(Ctx& c, int layer) {
+inline void note_epilogue(Ctx& c, int layer, cudaStream_t st) {
   c.epi_launches[layer % kScratchBufs] += 1u;
-  c.last_kind = kLaunchEpilogue;
-  c.last_layer = layer;
+  c.history.epilogue(layer, st);
 }
-inline void note_apply(Ctx& c) { c.last_kind = kLaunchApply; }
-inline void note_inputs(Ctx& c) { c.last_kind = kLaunchInputs; }
-// Kernels launched without early start (they never let a successor start
-// before they complete).
-inline void note_other(Ctx& c) { c.last_kind = kLaunchOther; }
 
 // workspace layout (host)
 bool has_ring(const kvevict_config& c);

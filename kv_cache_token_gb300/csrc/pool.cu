@@ -957,18 +957,18 @@ cudaError_t launch_decode(Ctx& ctx, int layer, const void* q, const void* k_new,
   if (q) {
     e = launch_attend(ctx, layer, q, k_new, v_new, stream, true);
     if (e != cudaSuccess) return e;
-    note_attend(ctx, layer);
+    ctx.history.attend(layer, stream);
   }
   bool apply_kernel = false;
   e = launch_epilogue(ctx, layer, q != nullptr, new_pos, k_new, v_new, out, lse, victims, n_victims, stream,
                       &apply_kernel);
   if (e != cudaSuccess) return e;
-  note_epilogue(ctx, layer);
+  note_epilogue(ctx, layer, stream);
   // every lane of the layer is now within its budget
   ctx.layer_steady[layer] = true;
   if (!apply_kernel) return e;
   e = launch_allocate_apply(ctx, layer, k_new, v_new, false, nullptr, stream, false);
-  note_apply(ctx);
+  ctx.history.apply(stream);
   return e;
 }
 

@@ -1,0 +1,55 @@
+"""Calls on several streams: results are those of the same calls one after
+another."""
+import pytest
+import torch
+
+from kv_cache_token_gb300 import BF16, Engine, H2O, config_from
+
+pytestmark = pytest.mark.gpu
+
+
+def decode_engine(B, Hq, Hkv, d, n, L):
+    eng = Engine(config_from(policy=H2O, num_layers=L, batch=B, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=d, kv_dtype=BF16,
+                             blocks_per_pool=B * Hkv * ((n + 12) // 16 + 2), max_tokens=n + 12, budget=128, recent_window=32,
+                             obs_window=1, pool_kernel=1))
+    eng.reset()
+    return eng
+
+
+def test_a_cache_call_on_a_second_stream_between_projection_and_decode_step():
+    """norm_rope on one stream, kv4_write of its new row on a second, the
+    decode step on the first: the step reads the finished rows."""
+    B, Hq, Hkv, d, n, L = 2, 16, 2, 128, 200, 2
+    a, b = decode_engine(B, Hq, Hkv, d, n, L), decode_engine(B, Hq, Hkv, d, n, L)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    for l in range(L):
+        k, v = rnd(B, Hkv, n, d), rnd(B, Hkv, n, d)
+        a.prefill(l, k, v)
+        b.prefill(l, k, v)
+    c = a.kv4_cache(B * Hkv * 2, 2)
+    starts = torch.zeros((B * Hkv,), dtype=torch.int32, device="cuda")
+    sq = [torch.empty((B, h, 1, d), dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv, Hkv)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for t in range(6):
+        for l in range(L):
+            x = rnd(B, 1, (Hq + 2 * Hkv) * d)
+            q, k, v = b.norm_rope(x, pos0=n + t)
+            torch.cuda.synchronize()
+            ref = [r.clone() for r in b.decode_step(l, q.view(B, Hq, d), k.view(B, Hkv, d), v.view(B, Hkv, d), n + t)]
+            for o in sq:
+                o.zero_()
+            torch.cuda.synchronize()
+            a.norm_rope(x, pos0=n + t, q=sq[0], k=sq[1], v=sq[2])
+            side.wait_stream(torch.cuda.current_stream())
+            a.kv4_write(c, starts, sq[1], sq[2], stream=side)
+            got = a.decode_step(l, sq[0].view(B, Hq, d), sq[1].view(B, Hkv, d), sq[2].view(B, Hkv, d), n + t)
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+            gk, gv = a.kv4_read(c, starts, 1)
+            b_c = b.kv4_cache(B * Hkv * 2, 2)
+            b.kv4_write(b_c, starts, k, v)
+            rk, rv = b.kv4_read(b_c, starts, 1)
+            assert torch.equal(gk, rk) and torch.equal(gv, rv)
+    assert a.last_error()[0] == 0 and b.last_error()[0] == 0
