@@ -471,7 +471,8 @@ kvevict_status kvevict_kv4_pack(kvevict_ctx* ctx, int layer, const kvevict_kv4* 
 
 /* Reads values back: tokens starts[lane] .. starts[lane] + n - 1 (NULL: from
  * 0) into k and v [B][Hkv][n][d] (bf16, device, 16-byte aligned), rounded
- * once, as kvevict_prefill takes them.  Rows of tokens at or past lens[lane]
+ * once, as kvevict_prefill takes them (n = 1: the k_new, v_new of
+ * kvevict_decode_step).  Rows of tokens at or past lens[lane]
  * (int32 [B*Hkv], device; NULL: the table's end) are left as they were, as are
  * the rows of a lane whose start is below 0 and of a page id out of range
  * (both reported: index out of range). */

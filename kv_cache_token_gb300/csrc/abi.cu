@@ -590,8 +590,8 @@ kvevict_status kvevict_kv4_read(kvevict_ctx* ctx, const kvevict_kv4* cache, cons
   if (s != KVEVICT_OK) return s;
   if (n < 1 || !k || !v || !aligned16(k) || !aligned16(v) || !aligned4(starts) || !aligned4(lens))
     return KVEVICT_E_INVALID_ARG;
-  return launched(ctx, stream, kve::launch_kv4_read(ctx->c, *cache, starts, lens, n, k, v,
-                                                    static_cast<cudaStream_t>(stream)));
+  ctx->c.history.inputs(stream);     // a row read back may be a decode step's new row
+  return cuda_status(kve::launch_kv4_read(ctx->c, *cache, starts, lens, n, k, v, static_cast<cudaStream_t>(stream)));
 }
 
 kvevict_status kvevict_kv4_attend(kvevict_ctx* ctx, const kvevict_kv4* cache, const int32_t* lens, const void* q,

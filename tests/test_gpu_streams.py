@@ -53,3 +53,35 @@ def test_a_cache_call_on_a_second_stream_between_projection_and_decode_step():
             rk, rv = b.kv4_read(b_c, starts, 1)
             assert torch.equal(gk, rk) and torch.equal(gv, rv)
     assert a.last_error()[0] == 0 and b.last_error()[0] == 0
+
+
+def test_a_row_read_back_feeds_the_decode_step():
+    """kv4_read's row is the new row of the decode step launched right after
+    it, layer after layer."""
+    B, Hq, Hkv, d, n, L = 2, 16, 2, 128, 200, 3
+    a, b = decode_engine(B, Hq, Hkv, d, n, L), decode_engine(B, Hq, Hkv, d, n, L)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    for l in range(L):
+        k, v = rnd(B, Hkv, n, d), rnd(B, Hkv, n, d)
+        a.prefill(l, k, v)
+        b.prefill(l, k, v)
+    c = a.kv4_cache(B * Hkv * 2, 2)
+    k, v = rnd(B, Hkv, 24, d), rnd(B, Hkv, 24, d)
+    a.kv4_write(c, None, k, v)
+    kn, vn = [torch.empty((B, Hkv, 1, d), dtype=torch.bfloat16, device="cuda") for _ in (0, 1)]
+    for t in range(8):
+        for l in range(L):
+            at = torch.full((B * Hkv,), 3 * t + l, dtype=torch.int32, device="cuda")
+            q = rnd(B, Hq, d)
+            rk, rv = a.kv4_read(c, at, 1)
+            torch.cuda.synchronize()
+            ref = [r.clone() for r in b.decode_step(l, q, rk.view(B, Hkv, d), rv.view(B, Hkv, d), n + t)]
+            kn.zero_()
+            vn.zero_()
+            torch.cuda.synchronize()
+            a.kv4_read(c, at, 1, k=kn, v=vn)
+            got = a.decode_step(l, q, kn.view(B, Hkv, d), vn.view(B, Hkv, d), n + t)
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    assert a.last_error()[0] == 0 and b.last_error()[0] == 0

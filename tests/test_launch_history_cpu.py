@@ -1,6 +1,7 @@
 """Which decode kernels may start before the kernel in front of them: the
 launch history's rules, compiled for the host."""
 import os
+import re
 import shutil
 import subprocess
 
@@ -88,3 +89,14 @@ def test_launch_history_rules(tmp_path):
     subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", "-Werror", "-pthread", "-I", CSRC, str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout
+
+
+def test_calls_that_write_a_steps_rows_hold_its_stream():
+    """The calls whose outputs a decode step reads are noted as such, the
+    others as ordinary: each entry point's own line."""
+    src = open(os.path.join(CSRC, "abi.cu")).read()
+    body = lambda f: re.search(r"kvevict_status %s\(.*?\n}" % f, src, re.S).group(0)
+    for f in ("kvevict_norm_rope", "kvevict_kv4_read"):
+        assert "history.inputs(stream)" in body(f) and "launched(" not in body(f)
+    for f in ("kvevict_attend_prompt", "kvevict_kv4_write", "kvevict_kv4_pack", "kvevict_kv4_attend"):
+        assert "launched(ctx, stream" in body(f)
