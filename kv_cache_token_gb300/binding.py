@@ -262,6 +262,18 @@ class Engine:
             _LIB.kvevict_destroy(h)
             self.h = None
 
+    def _new(self, stream, shape, dtype, make=None):
+        """A default output of a call on `stream` (None: the current one).  Its
+        memory and its fill are that stream's, as the kernel that writes it is;
+        the current stream, where the caller may read it, is noted as a user."""
+        make = make or torch.empty
+        if stream is None:
+            return make(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            t = make(shape, dtype=dtype, device=self.device)
+        t.record_stream(torch.cuda.current_stream(self.device))
+        return t
+
     # ---- C-ABI calls ----------------------------------------------------------
     def reset(self, stream=None):
         _check(lib().kvevict_reset(self.h, _stream(stream)), "kvevict_reset")
@@ -280,9 +292,9 @@ class Engine:
                     n_victims=None, stream=None):
         c = self.cfg
         if q is not None and out is None:
-            out = torch.empty((c.batch, c.num_q_heads, c.head_dim), dtype=torch.float32, device=self.device)
+            out = self._new(stream, (c.batch, c.num_q_heads, c.head_dim), torch.float32)
         if q is not None and lse is None:
-            lse = torch.empty((c.batch, c.num_q_heads), dtype=torch.float32, device=self.device)
+            lse = self._new(stream, (c.batch, c.num_q_heads), torch.float32)
         victims = self.victims if victims is None else victims
         n_victims = self.n_victims if n_victims is None else n_victims
         for t in (q, k_new, v_new):
@@ -300,9 +312,9 @@ class Engine:
                     stream=None):
         c = self.cfg
         if q is not None and out is None:
-            out = torch.empty((c.batch, c.num_q_heads, c.head_dim), dtype=torch.float32, device=self.device)
+            out = self._new(stream, (c.batch, c.num_q_heads, c.head_dim), torch.float32)
         if q is not None and lse is None:
-            lse = torch.empty((c.batch, c.num_q_heads), dtype=torch.float32, device=self.device)
+            lse = self._new(stream, (c.batch, c.num_q_heads), torch.float32)
         victims = self.victims if victims is None else victims
         n_victims = self.n_victims if n_victims is None else n_victims
         _check(lib().kvevict_finish_step(self.h, layer, _ptr(q), _ptr(k_new), _ptr(v_new), int(new_pos),
@@ -315,9 +327,9 @@ class Engine:
         library's built-in scratch array (no workspace, no allocation inside)."""
         c = self.cfg
         if out is None:
-            out = torch.empty((c.batch, c.num_q_heads, c.head_dim), dtype=torch.float32, device=self.device)
+            out = self._new(stream, (c.batch, c.num_q_heads, c.head_dim), torch.float32)
         if lse is None:
-            lse = torch.empty((c.batch, c.num_q_heads), dtype=torch.float32, device=self.device)
+            lse = self._new(stream, (c.batch, c.num_q_heads), torch.float32)
         _check(lib().kvevict_attend_static(self.h, layer, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(out), _ptr(lse),
                                            _stream(stream)), "kvevict_attend_static")
         return out, lse
@@ -330,11 +342,11 @@ class Engine:
             return None
         w = q_win.shape[2]
         if lse is None:
-            lse = torch.empty((c.batch, c.num_q_heads, w), dtype=torch.float32, device=self.device)
+            lse = self._new(stream, (c.batch, c.num_q_heads, w), torch.float32)
         if a_out is None:
-            a_out = torch.empty((c.batch, c.num_q_heads, w, c.head_dim), dtype=torch.float32, device=self.device)
+            a_out = self._new(stream, (c.batch, c.num_q_heads, w, c.head_dim), torch.float32)
         if scores is None:
-            scores = torch.zeros((self.lanes, c.max_tokens), dtype=torch.float32, device=self.device)
+            scores = self._new(stream, (self.lanes, c.max_tokens), torch.float32, torch.zeros)
         assert q_win.is_contiguous() and q_pos.dtype == torch.int32
         _check(lib().kvevict_score(self.h, layer, _ptr(q_win), w, _ptr(q_pos), _ptr(lse), _ptr(a_out),
                                    _ptr(scores), _stream(stream)), "kvevict_score")
@@ -350,9 +362,9 @@ class Engine:
             return None
         w = q_win.shape[2]
         if lse is None:
-            lse = torch.empty((c.batch, c.num_q_heads, w), dtype=torch.float32, device=self.device)
+            lse = self._new(stream, (c.batch, c.num_q_heads, w), torch.float32)
         if scores is None:
-            scores = torch.zeros((self.lanes, c.max_tokens), dtype=torch.float32, device=self.device)
+            scores = self._new(stream, (self.lanes, c.max_tokens), torch.float32, torch.zeros)
         assert q_win.is_contiguous() and q_pos.dtype == torch.int32
         _check(lib().kvevict_score_mass(self.h, layer, _ptr(q_win), w, _ptr(q_pos), kind, _ptr(lse),
                                         _ptr(scores), _stream(stream)), "kvevict_score_mass")
@@ -363,9 +375,9 @@ class Engine:
         n_lanes, stride = keys.shape
         kd = KEY_F64 if keys.dtype == torch.float64 else KEY_F32
         if victims is None:
-            victims = torch.full((n_lanes, stride), -1, dtype=torch.int32, device=self.device)
+            victims = self._new(stream, (n_lanes, stride), torch.int32, lambda *a, **kw: torch.full(*a, -1, **kw))
         if n_victims is None:
-            n_victims = torch.zeros((n_lanes,), dtype=torch.int32, device=self.device)
+            n_victims = self._new(stream, (n_lanes,), torch.int32, torch.zeros)
         assert keys.is_contiguous() and positions.is_contiguous() and positions.shape == keys.shape
         _check(lib().kvevict_select(self.h, _ptr(keys), kd, _ptr(positions), _ptr(counts), n_lanes, stride,
                                     budget, recent_window, _ptr(victims), _ptr(n_victims), _stream(stream)),
@@ -377,13 +389,13 @@ class Engine:
         c = self.cfg
         # the library writes freed[0..n_freed) and moves[0..n_moves) and both counts
         if freed is None:
-            freed = torch.empty((c.blocks_per_pool,), dtype=torch.int32, device=self.device)
+            freed = self._new(stream, (c.blocks_per_pool,), torch.int32)
         if n_freed is None:
-            n_freed = torch.empty((1,), dtype=torch.int32, device=self.device)
+            n_freed = self._new(stream, (1,), torch.int32)
         if moves is None:
-            moves = torch.empty((self.lanes * c.max_tokens, 6), dtype=torch.int32, device=self.device)
+            moves = self._new(stream, (self.lanes * c.max_tokens, 6), torch.int32)
         if n_moves is None:
-            n_moves = torch.empty((1,), dtype=torch.int32, device=self.device)
+            n_moves = self._new(stream, (1,), torch.int32)
         _check(lib().kvevict_compact(self.h, layer, _ptr(victims), _ptr(n_victims), _ptr(freed), _ptr(n_freed),
                                      _ptr(moves), _ptr(n_moves), _stream(stream)), "kvevict_compact")
         return freed, n_freed, moves, n_moves
@@ -396,13 +408,13 @@ class Engine:
         """kvevict_relocate on `stream`; returns (freed, n_freed, moves, n_moves)."""
         c = self.cfg
         if freed is None:
-            freed = torch.empty((c.blocks_per_pool,), dtype=torch.int32, device=self.device)
+            freed = self._new(stream, (c.blocks_per_pool,), torch.int32)
         if n_freed is None:
-            n_freed = torch.empty((1,), dtype=torch.int32, device=self.device)
+            n_freed = self._new(stream, (1,), torch.int32)
         if moves is None:
-            moves = torch.empty((self.lanes * c.max_tokens, 6), dtype=torch.int32, device=self.device)
+            moves = self._new(stream, (self.lanes * c.max_tokens, 6), torch.int32)
         if n_moves is None:
-            n_moves = torch.empty((1,), dtype=torch.int32, device=self.device)
+            n_moves = self._new(stream, (1,), torch.int32)
         _check(lib().kvevict_relocate(self.h, layer, _ptr(freed), _ptr(n_freed), _ptr(moves), _ptr(n_moves),
                                       _stream(stream)), "kvevict_relocate")
         return freed, n_freed, moves, n_moves
@@ -427,7 +439,7 @@ class Engine:
                 _dense(w, (d,), dt, dev, "a norm weight")
         if pos is not None:
             _dense(pos, (n,), torch.int32, dev, "pos")
-        out = lambda t, h: torch.empty((B, h, n, d), dtype=dt, device=dev) if t is None else t
+        out = lambda t, h: self._new(stream, (B, h, n, d), dt) if t is None else t
         q, k, v = out(q, Hq), out(k, Hkv), out(v, Hkv)
         _dense(q, (B, Hq, n, d), dt, dev, "q")
         _dense(k, (B, Hkv, n, d), dt, dev, "k")
@@ -448,9 +460,9 @@ class Engine:
         _dense(k, (B, Hkv, n, d), bf, dev, "k")
         _dense(v, (B, Hkv, n, d), bf, dev, "v")
         if out is None:
-            out = torch.empty((B, n, Hq, d), dtype=bf, device=dev)
+            out = self._new(stream, (B, n, Hq, d), bf)
         if lse is None:
-            lse = torch.empty((B, Hq, n), dtype=torch.float32, device=dev)
+            lse = self._new(stream, (B, Hq, n), torch.float32)
         _dense(out, (B, n, Hq, d), bf, dev, "out")
         _dense(lse, (B, Hq, n), torch.float32, dev, "lse")
         _check(lib().kvevict_attend_prompt(self.h, q.data_ptr(), k.data_ptr(), v.data_ptr(), n, sinks, window,
@@ -493,8 +505,8 @@ class Engine:
         c, ref = self.cfg, self._cache_ref(cache)
         shp = (c.batch, c.num_kv_heads, n, c.head_dim)
         # rows past a lane's end are not written
-        k = torch.zeros(shp, dtype=torch.bfloat16, device=self.device) if k is None else k
-        v = torch.zeros(shp, dtype=torch.bfloat16, device=self.device) if v is None else v
+        k = self._new(stream, shp, torch.bfloat16, torch.zeros) if k is None else k
+        v = self._new(stream, shp, torch.bfloat16, torch.zeros) if v is None else v
         _dense(k, shp, torch.bfloat16, self.device, "k")
         _dense(v, shp, torch.bfloat16, self.device, "v")
         _check(lib().kvevict_kv4_read(self.h, ref, self._lane_ints(starts, "starts"),
@@ -508,9 +520,9 @@ class Engine:
         shp = (c.batch, c.num_q_heads, c.head_dim)
         _dense(q, shp, torch.bfloat16, dev, "q")
         if out is None:
-            out = torch.empty(shp, dtype=torch.bfloat16, device=dev)
+            out = self._new(stream, shp, torch.bfloat16)
         if lse is None:
-            lse = torch.empty(shp[:2], dtype=torch.float32, device=dev)
+            lse = self._new(stream, shp[:2], torch.float32)
         _dense(out, shp, torch.bfloat16, dev, "out")
         _dense(lse, shp[:2], torch.float32, dev, "lse")
         _need(lens is not None, "lens")
@@ -520,7 +532,7 @@ class Engine:
         return out, lse
 
     def stats(self, layer, stream=None):
-        out = torch.zeros((NSTATS,), dtype=torch.int64, device=self.device)
+        out = self._new(stream, (NSTATS,), torch.int64, torch.zeros)
         _check(lib().kvevict_stats(self.h, layer, _ptr(out), _stream(stream)), "kvevict_stats")
         return out
 

@@ -75,3 +75,82 @@ def test_a_cache_on_another_device_is_refused(B):
     b.kv4_geometry = B.kv4_geometry(b.cfg, b.device)
     with pytest.raises(ValueError, match="cache was made for"):
         a.kv4_pack(0, bare_cache(B, b))
+
+
+class _Recorder:
+    """Stands in for torch in the binding: allocations are real (on the CPU)
+    and noted with the stream that was current."""
+
+    def __init__(self):
+        self.current, self.made, self.users = "main", [], []
+        self.cuda = self
+
+    def __getattr__(self, name):
+        return getattr(torch, name)
+
+    def stream(self, s):
+        import contextlib
+
+        @contextlib.contextmanager
+        def on():
+            before, self.current = self.current, s
+            yield
+            self.current = before
+        return on()
+
+    def current_stream(self, device=None):
+        return self.current
+
+    def _make(self, t):
+        self.made.append((self.current, t))
+        t.record_stream = self.users.append
+        return t
+
+    def empty(self, shape, dtype=None, device=None):
+        return self._make(torch.empty(shape, dtype=dtype))
+
+    def zeros(self, shape, dtype=None, device=None):
+        return self._make(torch.zeros(shape, dtype=dtype))
+
+    def full(self, shape, value, dtype=None, device=None):
+        return self._make(torch.full(shape, value, dtype=dtype))
+
+
+class _Stream:
+    cuda_stream = 7
+
+
+@pytest.mark.parametrize("call, outputs", [
+    (lambda e, c, t, s: e.norm_rope(t(2, 3, 12 * 128), stream=s), 3),
+    (lambda e, c, t, s: e.attend_prompt(t(2, 8, 3, 128), t(2, 2, 3, 128), t(2, 2, 3, 128), stream=s), 2),
+    (lambda e, c, t, s: e.kv4_read(c, None, 4, stream=s), 2),
+    (lambda e, c, t, s: e.kv4_attend(c, torch.zeros(4, dtype=torch.int32), t(2, 8, 128), stream=s), 2),
+    (lambda e, c, t, s: e.decode_step(0, t(2, 8, 128), t(2, 2, 128), t(2, 2, 128), 0, stream=s), 2),
+    (lambda e, c, t, s: e.finish_step(0, t(2, 8, 128), t(2, 2, 128), t(2, 2, 128), 0, stream=s), 2),
+    (lambda e, c, t, s: e.attend_static(0, t(2, 8, 128), t(2, 2, 128), t(2, 2, 128), stream=s), 2),
+    (lambda e, c, t, s: e.score(0, t(2, 8, 4, 128), torch.zeros(4, dtype=torch.int32), stream=s), 3),
+    (lambda e, c, t, s: e.score_mass(0, t(2, 8, 4, 128), torch.zeros(4, dtype=torch.int32), 0, stream=s), 2),
+    (lambda e, c, t, s: e.select(torch.zeros(4, 16), torch.zeros((4, 16), dtype=torch.int32),
+                                 torch.zeros(4, dtype=torch.int32), 8, 2, stream=s), 2),
+    (lambda e, c, t, s: e.compact(0, None, None, stream=s), 4),
+    (lambda e, c, t, s: e.relocate(0, stream=s), 4),
+    (lambda e, c, t, s: e.stats(0, stream=s), 1)])
+def test_default_outputs_belong_to_the_calls_stream(B, monkeypatch, call, outputs):
+    """Outputs that a call makes itself are allocated and filled on the stream
+    its kernel runs on: a fill on another one may land after the kernel."""
+    import types
+    e = bare_engine(B)
+    c = bare_cache(B, e)
+    e.device = types.SimpleNamespace(index=-1)          # tensors of this test are the CPU's
+    e.victims = e.n_victims = torch.zeros(4, dtype=torch.int32)
+    rec, s = _Recorder(), _Stream()
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 0
+    monkeypatch.setattr(B, "torch", rec)
+    monkeypatch.setattr(B, "lib", lambda: Lib())
+    call(e, c, lambda *shape: torch.zeros(shape, dtype=torch.bfloat16), s)
+    assert len(rec.made) == outputs
+    assert all(on is s for on, _ in rec.made)
+    assert rec.users == ["main"] * outputs              # and kept while the current stream may read them

@@ -85,3 +85,42 @@ def test_a_row_read_back_feeds_the_decode_step():
             torch.cuda.synchronize()
             assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
     assert a.last_error()[0] == 0 and b.last_error()[0] == 0
+
+
+def test_outputs_made_by_a_call_on_a_second_stream():
+    """While the current stream is busy, calls on a second stream make their
+    own outputs: nothing queued on the current one lands in them later."""
+    eng = Engine(config_from(policy=H2O, num_layers=1, batch=2, num_q_heads=8, num_kv_heads=2, head_dim=128, kv_dtype=BF16,
+                             blocks_per_pool=4, max_tokens=8, budget=4, recent_window=2, obs_window=1, pool_kernel=1))
+    eng.reset()
+    g = torch.Generator(device="cuda").manual_seed(9)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    c = eng.kv4_cache(4 * 8, 8)
+    k, v, q, lens = rnd(2, 2, 100, 128), rnd(2, 2, 100, 128), rnd(2, 8, 128), torch.full((4,), 100, dtype=torch.int32).cuda()
+    x, pq = rnd(2, 100, 12 * 128), rnd(2, 8, 100, 128)
+    eng.kv4_write(c, None, k, v)
+    calls = [lambda **kw: eng.kv4_read(c, None, 100, **kw), lambda **kw: eng.kv4_attend(c, lens, q, **kw),
+             lambda **kw: eng.norm_rope(x, **kw), lambda **kw: eng.attend_prompt(pq, k, v, **kw)]
+    ref = [f() for f in calls]
+    a = torch.randn((8192, 8192), device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+    # blocks the allocator would hand out again while the current stream still writes them
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for _ in range(20):
+            a = (a @ a).clamp_(-1, 1)
+        old = [[torch.empty_like(t) for t in r] for r in ref]
+        for r in old:
+            for t in r:
+                t.fill_(9.0)
+        del old, r, t
+        got = [f(stream=side) for f in calls]
+        side.synchronize()
+        for r, o in zip(ref, got):
+            for s, t in zip(r, o):
+                assert torch.equal(s, t)
+        torch.cuda.synchronize()
+        for r, o in zip(ref, got):
+            for s, t in zip(r, o):
+                assert torch.equal(s, t)
+    assert eng.last_error()[0] == 0
