@@ -368,7 +368,8 @@ kvevict_status kvevict_attend_static(kvevict_ctx* ctx, int layer, const void* q,
  * engine state.  The context's device must be current and the stream one of
  * its streams (KVEVICT_E_INVALID_ARG for another device).  Outputs must not
  * overlap inputs.  int32 and fp32 arrays are 4-byte aligned
- * (KVEVICT_E_INVALID_ARG otherwise). */
+ * (KVEVICT_E_INVALID_ARG otherwise).  Several host threads may make these
+ * calls on one context at once; the calls above come from one at a time. */
 
 /* Per-head norm and rotation of a projection, written in the layouts of the
  * other calls.  qkv holds one row per token, batch_stride elements from

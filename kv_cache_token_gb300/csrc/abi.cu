@@ -288,8 +288,6 @@ kvevict_status kvevict_create(const kvevict_config* cfg, const kvevict_buffers* 
   ctx->c.device = dev;
   for (int c = 0; c < kve::kScratchBufs; ++c) ctx->c.epi_launches[c] = 0u;
   ctx->c.tmaps = nullptr;
-  ctx->c.rope_base = 0.0;
-  ctx->c.rope_dim = -1;
   ctx->c.layer_budget = new (std::nothrow) int[cfg->num_layers];
   ctx->c.layer_recent = new (std::nothrow) int[cfg->num_layers];
   ctx->c.layer_steady = new (std::nothrow) bool[cfg->num_layers];

@@ -19,7 +19,6 @@ constexpr int kMaxW = 64;           // largest SnapKV obsWindow supported
 constexpr int kMaxG = 16;           // largest GQA group
 constexpr int kAttendWarps = 4;     // warps per CTA of the decode kernel
 constexpr int kStages = 3;          // copy stages per warp of the decode kernel
-constexpr int kRopePairs = 64;      // rotated pairs of a head at most
 constexpr int kScratchBufs = 3;     // copies of the decode split-K scratch (layer l uses copy l % 3)
 
 // device status bits (read and cleared by kvevict_last_error)
@@ -151,11 +150,6 @@ struct Ctx {
   // epilogue is the right kernel.  A performance hint only: both epilogue
   // kernels handle every case.
   bool* layer_steady;
-  // The rotation's turns per position of the last (base, rotary_dim) asked
-  // for, as 64-bit fractions (host; rope_dim -1: none yet).
-  double rope_base;
-  int rope_dim;
-  uint64_t rope_freq[kRopePairs];
 };
 
 inline void note_epilogue(Ctx& c, int layer, cudaStream_t st) {
@@ -200,7 +194,7 @@ cudaError_t launch_stats(const Ctx&, int layer, long long* out, cudaStream_t);
 cudaError_t launch_wait_check(const Ctx&, int polls, cudaStream_t);
 cudaError_t launch_attend_into(const Ctx&, int layer, const void* q, const void* k_new, const void* v_new,
                                float* logits, float* part_o, float* part_ml, int32_t* lane_nseg, cudaStream_t);
-cudaError_t launch_norm_rope(Ctx&, const void* qkv, long long batch_stride, long long row_stride, int n,
+cudaError_t launch_norm_rope(const Ctx&, const void* qkv, long long batch_stride, long long row_stride, int n,
                              const void* wq, const void* wk, float eps, const int32_t* pos, int pos0, int r,
                              double base, int interleaved, void* q, void* k, void* v, cudaStream_t);
 cudaError_t launch_attend_prompt(const Ctx&, const void* q, const void* k, const void* v, int n, int sinks,

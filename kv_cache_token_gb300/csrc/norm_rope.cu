@@ -18,17 +18,16 @@
 // the angle to 2^-32 turn whatever the position (an fp32 product p * w loses
 // 1e-2 rad at p = 10^5).  Sines and cosines are taken once per token and
 // shared by all its heads through shared memory.
-#include <cmath>
 #include <cstring>
 
 #include "kvevict_internal.cuh"
+#include "rope_turns.h"
 
 namespace kve {
 
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kMaxPairs = kRopePairs;
 constexpr int kUnroll = 3;
 
 struct RopeArgs {
@@ -40,7 +39,7 @@ struct RopeArgs {
   float eps;
   int n, pos0, r, interleaved, Hq, Hkv;
   int tok;             // tokens of a CTA
-  uint64_t freq[kMaxPairs];   // fractions of a turn per position
+  uint64_t freq[kRopePairs];   // fractions of a turn per position
 };
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -220,27 +219,9 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
   }
 }
 
-// Fractions of a turn per position of the r/2 pairs: base^(-2i/r) / 2 pi,
-// mod 1, in units of 2^-64.  base^(-2i/r) is the product of the factors of
-// i's bits, so the host takes at most 6 powers, not 64.
-void turn_fractions(double base, int r, uint64_t* f) {
-  constexpr double kTau = 6.283185307179586476925286766559;
-  double p[kMaxPairs];
-  p[0] = 1.0;
-  for (int i = 1; i < r / 2; ++i) {
-    const int low = i & -i;
-    p[i] = i == low ? std::pow(base, -2.0 * low / r) : p[i - low] * p[low];
-  }
-  for (int i = 0; i < r / 2; ++i) {
-    double t = p[i] / kTau;
-    t -= std::floor(t);
-    f[i] = t >= 1.0 ? 0ull : static_cast<unsigned long long>(t * 18446744073709551616.0);
-  }
-}
-
 }  // namespace
 
-cudaError_t launch_norm_rope(Ctx& ctx, const void* qkv, long long batch_stride, long long row_stride, int n,
+cudaError_t launch_norm_rope(const Ctx& ctx, const void* qkv, long long batch_stride, long long row_stride, int n,
                              const void* wq, const void* wk, float eps, const int32_t* pos, int pos0, int r,
                              double base, int interleaved, void* q, void* k, void* v, cudaStream_t st) {
   const Dims& dm = ctx.dims;
@@ -255,13 +236,7 @@ cudaError_t launch_norm_rope(Ctx& ctx, const void* qkv, long long batch_stride, 
   a.v = static_cast<unsigned char*>(v);
   a.eps = eps; a.n = n; a.pos0 = pos0; a.r = r; a.interleaved = interleaved;
   a.Hq = dm.Hq; a.Hkv = dm.Hkv;
-  // a model asks for one base: its table is kept from call to call
-  if (ctx.rope_base != base || ctx.rope_dim != r) {
-    turn_fractions(base, r, ctx.rope_freq);
-    ctx.rope_base = base;
-    ctx.rope_dim = r;
-  }
-  memcpy(a.freq, ctx.rope_freq, sizeof(a.freq));
+  memcpy(a.freq, turn_table(base, r), sizeof(a.freq));
   // A CTA takes up to eight tokens, which share its start (angles, norm
   // weights) and overlap loads with work, as long as there are CTAs for two
   // on every SM (32768 tokens: 137 us, against 228 with a token a CTA; 2331

@@ -3,7 +3,7 @@ another."""
 import pytest
 import torch
 
-from kv_cache_token_gb300 import BF16, Engine, H2O, config_from
+from kv_cache_token_gb300 import BF16, Engine, H2O, config_from, lib
 
 pytestmark = pytest.mark.gpu
 
@@ -123,4 +123,42 @@ def test_outputs_made_by_a_call_on_a_second_stream():
         for r, o in zip(ref, got):
             for s, t in zip(r, o):
                 assert torch.equal(s, t)
+    assert eng.last_error()[0] == 0
+
+
+def test_host_threads_with_bases_of_their_own():
+    """Projections of several models' layers, a host thread and a stream each,
+    on one engine: every call turns by its own base."""
+    import ctypes
+    import threading
+    eng = Engine(config_from(policy=H2O, num_layers=1, batch=1, num_q_heads=4, num_kv_heads=2, head_dim=128, kv_dtype=BF16,
+                             blocks_per_pool=4, max_tokens=8, budget=4, recent_window=2, obs_window=1, pool_kernel=1))
+    eng.reset()
+    x = torch.randn((1, 1, 8 * 128), device="cuda").bfloat16()
+    bases = [(1e4, 128), (5e5, 96), (1e6, 112), (2e4, 64)]
+    ref = [eng.norm_rope(x, pos0=1000, base=b, rotary_dim=r)[0].clone() for b, r in bases]
+    torch.cuda.synchronize()
+    assert all(not torch.equal(ref[i], ref[j]) for i in range(4) for j in range(i))
+    wrong, codes, gate, call = [0] * 4, [0] * 4, threading.Barrier(4), lib().kvevict_norm_rope
+    P = lambda t: ctypes.c_void_p(t.data_ptr())
+
+    def work(i):
+        s = torch.cuda.Stream()
+        outs = [[torch.empty((1, h, 1, 128), dtype=torch.bfloat16, device="cuda") for h in (4, 2, 2)] for _ in range(200)]
+        torch.cuda.synchronize()
+        args = [(eng.h, P(x), 0, 1024, 1, None, None, 1e-6, None, 1000, bases[i][1], bases[i][0], 0, P(q), P(k), P(v),
+                 ctypes.c_void_p(s.cuda_stream)) for q, k, v in outs]
+        gate.wait()
+        for _ in range(40):
+            for a in args:
+                codes[i] |= call(*a)
+            s.synchronize()
+            wrong[i] += sum(not torch.equal(o[0], ref[i]) for o in outs)
+
+    t = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for th in t:
+        th.start()
+    for th in t:
+        th.join()
+    assert codes == [0] * 4 and wrong == [0] * 4, (codes, wrong)
     assert eng.last_error()[0] == 0

@@ -1,0 +1,45 @@
+"""The rotation's frequency tables, compiled for the host."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "kv_cache_token_gb300", "csrc")
+
+
+def run(tmp_path, main, *args):
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("g++ not available")
+    src, exe = tmp_path / "turns.cpp", tmp_path / "turns"
+    src.write_text("#include <cstdio>\n#include <cstdlib>\n#include <cstring>\n#include <thread>\n#include <vector>\n"
+                   "#include \"rope_turns.h\"\n" + main)
+    subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", "-Werror", "-pthread", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    return subprocess.run([str(exe), *map(str, args)], capture_output=True, text=True, timeout=120)
+
+
+def test_threads_with_bases_of_their_own(tmp_path):
+    r = run(tmp_path, r"""
+int main() {
+  std::vector<std::thread> t;
+  std::vector<int> wrong(8, 0);
+  for (int i = 0; i < 8; ++i)
+    t.emplace_back([&, i] {
+      for (int k = 0; k < 5000; ++k) {
+        // one base more than a thread keeps, taken in turn, and one asked for again
+        const double base = 10000.0 * (i + 1) + k % 5;
+        const int r = 16 * (1 + (i + k % 5) % 8);
+        uint64_t ref[kve::kRopePairs];
+        kve::turn_fractions(base, r, ref);
+        for (int again = 0; again < 2; ++again)
+          if (std::memcmp(ref, kve::turn_table(base, r), r / 2 * sizeof(uint64_t)) != 0) ++wrong[i];
+      }
+    });
+  for (auto& x : t) x.join();
+  for (int w : wrong)
+    if (w) return 1;
+  return 0;
+}
+""")
+    assert r.returncode == 0
