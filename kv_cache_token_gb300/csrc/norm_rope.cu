@@ -13,11 +13,12 @@
 // once, 805 MB, in 137 us: 5.9 TB/s, 0.87 of the measured copy bandwidth.
 //
 // Angle of pair i at position p: turns = p * f_i mod 1 with
-// f_i = base^(-2i/r) / 2 pi held as a 64-bit fraction of a turn, so the
-// product of the low 64 bits is the exact remainder and its top 32 bits give
-// the angle to 2^-32 turn whatever the position (an fp32 product p * w loses
-// 1e-2 rad at p = 10^5).  Sines and cosines are taken once per token and
-// shared by all its heads through shared memory.
+// f_i = base^(-2i/r) / 2 pi held as a 64-bit fraction of a turn, so the low 64
+// bits of the product are its remainder (an fp32 product p * w loses 1e-2 rad at
+// p = 10^5; what f_i itself is off by is in rope_turns.h).  Its top 32 bits,
+// rounded to fp32, give the angle to 2^-26 turn whatever the position.  Sines
+// and cosines are taken once per token and shared by all its heads through
+// shared memory.
 #include <cstring>
 
 #include "kvevict_internal.cuh"

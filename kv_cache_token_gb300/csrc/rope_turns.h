@@ -11,18 +11,25 @@ constexpr int kRopePairs = 64;      // rotated pairs of a head at most
 // Fractions of a turn per position of the r/2 pairs: base^(-2i/r) / 2 pi,
 // mod 1, in units of 2^-64.  base^(-2i/r) is the product of the factors of
 // i's bits, so the host takes at most 6 powers, not 64.
+//
+// In long double (64 bits on x86, 113 on Arm; doubles left 2^-24 turn at
+// position 2^31).  With 64 bits the powers are off by an ulp, 2^-63, each, the
+// products, the exponent and the division by 2^-64: at most 20 * 2^-64 of
+// 1 / 2 pi for bases from 1, and 2^-64 for the fraction's end, under 2^-61 turn
+// a position; 2^-30 at position 2^31.  Below base 1 the frequencies, and their
+// error with them, grow to 1 / base times that.
 inline void turn_fractions(double base, int r, uint64_t* f) {
-  constexpr double kTau = 6.283185307179586476925286766559;
-  double p[kRopePairs];
-  p[0] = 1.0;
+  constexpr long double kTau = 6.283185307179586476925286766559005768L;
+  long double p[kRopePairs];
+  p[0] = 1.0L;
   for (int i = 1; i < r / 2; ++i) {
     const int low = i & -i;
-    p[i] = i == low ? std::pow(base, -2.0 * low / r) : p[i - low] * p[low];
+    p[i] = i == low ? std::pow(static_cast<long double>(base), -2.0L * low / r) : p[i - low] * p[low];
   }
   for (int i = 0; i < r / 2; ++i) {
-    double t = p[i] / kTau;
+    long double t = p[i] / kTau;
     t -= std::floor(t);
-    f[i] = t >= 1.0 ? 0ull : static_cast<unsigned long long>(t * 18446744073709551616.0);
+    f[i] = t >= 1.0L ? 0ull : static_cast<unsigned long long>(t * 18446744073709551616.0L);
   }
 }
 

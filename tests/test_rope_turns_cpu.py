@@ -43,3 +43,25 @@ int main() {
 }
 """)
     assert r.returncode == 0
+
+
+@pytest.mark.parametrize("r", [16, 48, 96, 128])
+@pytest.mark.parametrize("base", [1.0, 1.5, 1e4, 5e5, 1e6, 1e300, 0.5, 1e-3])
+def test_tables_against_exact_arithmetic(tmp_path, base, r):
+    """A frequency is off by at most 2^-61 turn a position for bases from 1, and
+    1 / base times that below (the arithmetic is beside the function)."""
+    mp = pytest.importorskip("mpmath")
+    out = run(tmp_path, r"""
+int main(int, char** v) {
+  const int r = std::atoi(v[2]);
+  const uint64_t* f = kve::turn_table(std::atof(v[1]), r);
+  for (int i = 0; i < r / 2; ++i) std::printf("%llu\n", static_cast<unsigned long long>(f[i]));
+}
+""", repr(base), r)
+    with mp.workdps(80):
+        worst = mp.mpf(0)
+        for i, line in enumerate(out.stdout.split()):
+            t = mp.mpf(base) ** (mp.mpf(-2 * i) / r) / (2 * mp.pi)
+            d = mp.mpf(int(line)) / mp.mpf(2) ** 64 - t
+            worst = max(worst, abs(d - mp.nint(d)))
+        assert worst <= mp.mpf(2) ** -61 * max(1, 1 / base)
