@@ -52,6 +52,7 @@ constexpr int kMaxCtas = 256;          // parts the scratch holds: two a CTA
 constexpr int kJoinRounds = 3;         // what joining a lane's parts costs, in rounds
 constexpr float kBoost = 8.f;          // log2 of the largest u when m was set
 constexpr float kGrow = 6.f;           // m moves when some s + e exceeds it by more
+constexpr float kUnscale = 512.f;      // logits: 2^22 of the codes over 2^13 of the query
 
 struct Kv4Attend {
   const unsigned char* pages;
@@ -350,6 +351,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kThreads, 1) kv4_attend_kernel(
   // Query fragments in fp16, each head scaled by a power of two so that its
   // largest element is in [2^13, 2^14): exact but for elements below 2^-26 of
   // that one.  Elements that meet codes in bits 6-9 carry another 2^-4.
+  // (2^e of a head's largest element, e up to 127, is taken back by frag_c, the
+  // 2^9 left of the codes' 2^22 by kUnscale: together they would pass fp32.)
   auto load_q = [&](const unsigned char* qsm) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -365,7 +368,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kThreads, 1) kv4_attend_kernel(
       }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = max(-100, min(100, static_cast<int>(top >> 23) - 127));
+      const int e = max(-100, min(127, static_cast<int>(top >> 23) - 127));
       const float f = pow2(13 - e);
 #pragma unroll
       for (int w = 0; w < kG; ++w) {
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kThreads, 1) kv4_attend_kernel(
         const float q0 = __shfl_sync(0xffffffffu, sum, 8 * cq), q1 = __shfl_sync(0xffffffffu, sum, 8 * cq + 4);
         frag_s[(nt * kG + w) * 32] = make_float2(q0, q1);
       }
-      const float back = pow2(22 - 13 + e) * a.scale2;
+      const float back = pow2(e) * a.scale2;
       const float b0 = __shfl_sync(0xffffffffu, back, 8 * cq), b1 = __shfl_sync(0xffffffffu, back, 8 * cq + 4);
       frag_c[nt * 32] = make_float2(b0, b1);
     }
@@ -600,7 +603,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kThreads, 1) kv4_attend_kernel(
       for (int nt = 0; nt < NT; ++nt) {
         const float2 ch = frag_c[nt * 32];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[p][nt][e] = fmaf(z[p][nt][e], e & 1 ? ch.y : ch.x, e < 2 ? f0 : f1);
+        for (int e = 0; e < 4; ++e) z[p][nt][e] = fmaf(z[p][nt][e] * kUnscale, e & 1 ? ch.y : ch.x, e < 2 ? f0 : f1);
         if (!full) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)

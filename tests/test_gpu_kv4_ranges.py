@@ -1,0 +1,44 @@
+"""The 4-bit cache and its attention at the ends of their inputs' ranges."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving as S
+from tests import test_gpu_kv4 as T4
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("top", [99, 101, 103, 104, 110, 117, 118, 121, 124, 126, 127])
+def test_attend_queries_up_to_the_largest_number(d, top):
+    """Queries of 2^top against keys as small: logits of ordinary size, exact
+    in every step (one element of a head is not zero, keys are whole steps of
+    their scale), so out and lse follow the general bound without its cuts:
+    half a bf16 step, 2^-9 of sum p|v| for weights in fp16, 2^-20 (1 + |lse|)."""
+    eng = T4.engine(1, 4, 2, d)
+    n = 90
+    g = torch.Generator(device="cuda").manual_seed(top)
+    step = 2.0 ** (2 - top)
+    k = torch.zeros((2, n, d), device="cuda")
+    k[..., 5] = torch.randint(-7, 8, (2, n), generator=g, device="cuda").float() * step
+    k[..., 6] = 7 * step                                 # the group's scale is one step
+    v = torch.randn((2, n, d), generator=g, device="cuda")
+    q = torch.zeros((1, 4, d), device="cuda")
+    q[..., 5] = torch.tensor([1.0, -1.0, 1.5, -0.25], device="cuda") * 2.0 ** top
+    k, v, q = k.bfloat16(), v.bfloat16(), q.bfloat16()
+    assert torch.isfinite(q).all() and (k[..., 6] == 7 * step).all()
+    c = T4.shuffled(eng, 6)
+    eng.kv4_write(c, None, T4.shape4(eng, k), T4.shape4(eng, v))
+    hk, hv = T4.held(k, v)
+    out, lse = eng.kv4_attend(c, T4.ints(eng, [n, n - 7]), q)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    for l, m in enumerate((n, n - 7)):
+        hs = slice(2 * l, 2 * l + 2)
+        o, ls, mag, _ = S.attend_rows(T4.host(q)[0, hs], hk[l, :m], hv[l, :m])
+        assert np.abs(ls).max() < 60
+        # codes as subnormals cut the value products: 17 * (2^-15 + 2^-18) units of p * scale (see test_gpu_kv4)
+        unit = 17 * (2.0 ** -15 + 2.0 ** -18) / 6.97 * np.abs(hv[l, :m]).max()
+        assert (np.abs(T4.host(out)[0, hs] - o) <= 2.0 ** -8 * np.abs(o) + 2.0 ** -9 * mag + unit).all()
+        assert (np.abs(T4.host(lse)[0, hs] - ls) <= 2.0 ** -20 * (1 + np.abs(ls))).all()
+    assert eng.last_error()[0] == 0
