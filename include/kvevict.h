@@ -469,7 +469,9 @@ kvevict_status kvevict_kv4_write(kvevict_ctx* ctx, const kvevict_kv4* cache, con
 /* Stores every kept token of an engine layer, in kept order from index 0: the
  * lane then holds counts[lane] tokens (the layer's slice of buffers.counts).
  * A lane with more kept tokens than its table holds is left as it was and
- * reported. */
+ * reported (token table full), as is one whose count is not in 0..max_tokens
+ * (index out of range).  A token whose slot is outside the pool is stored as
+ * NaN and reported (index out of range). */
 kvevict_status kvevict_kv4_pack(kvevict_ctx* ctx, int layer, const kvevict_kv4* cache, void* stream);
 
 /* Reads values back: tokens starts[lane] .. starts[lane] + n - 1 (NULL: from

@@ -114,14 +114,20 @@ __global__ void __launch_bounds__(kKv4Threads, 5) kv4_store_kernel(Kv4Store a, i
       u[i] = make_uint4(0, 0, 0, 0);
       if (t >= start && t < end) {
         size_t row;
+        bool there = true;
         if (kPack) {
-          int s = a.slot[static_cast<size_t>(l) * a.cap + t];
-          if (s < 0 || s >= a.pool_rows) { set_status(a.status, ST_BAD_INDEX); s = 0; }
+          const int s = a.slot[static_cast<size_t>(l) * a.cap + t];
+          there = s >= 0 && s < a.pool_rows;
           row = s;
         } else {
           row = static_cast<size_t>(l) * a.n + (t - start);
         }
-        u[i] = *reinterpret_cast<const uint4*>((isv ? a.v : a.k) + row * D + (rem % kChunks) * 8);
+        if (there) {
+          u[i] = *reinterpret_cast<const uint4*>((isv ? a.v : a.k) + row * D + (rem % kChunks) * 8);
+        } else {      // no such row: the token holds NaN, not another's values
+          set_status(a.status, ST_BAD_INDEX);
+          u[i] = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+        }
       }
     }
   };

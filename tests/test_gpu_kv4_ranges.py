@@ -42,3 +42,39 @@ def test_attend_queries_up_to_the_largest_number(d, top):
         assert (np.abs(T4.host(out)[0, hs] - o) <= 2.0 ** -8 * np.abs(o) + 2.0 ** -9 * mag + unit).all()
         assert (np.abs(T4.host(lse)[0, hs] - ls) <= 2.0 ** -20 * (1 + np.abs(ls))).all()
     assert eng.last_error()[0] == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_pack_stores_no_other_tokens_row_for_a_slot_out_of_range(d):
+    """Table entries outside the pool: those tokens hold NaN and are reported;
+    the others, and lanes without such entries, are as always."""
+    n = 70
+    eng = T4.engine(2, 4, 2, d, blocks_per_pool=30, max_tokens=100, budget=90, recent_window=8)
+    k, v = T4.rows(4, n, d, 1), T4.rows(4, n, d, 2)
+    eng.prefill(0, T4.shape4(eng, k), T4.shape4(eng, v))
+    bad = {0: [0, 17, 69], 2: [31, 32, 33]}
+    rows = eng.cfg.blocks_per_pool * 16
+    for lane, at in bad.items():
+        eng.slots[0, lane, at] = torch.tensor([-1, rows, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    c = T4.shuffled(eng, 6)
+    eng.kv4_pack(0, c)
+    assert eng.last_error()[0] == 9
+    got = eng.kv4_read(c, None, n, lens=eng.counts[0])
+    for g, ref in zip(got, T4.held(k, v)):
+        g = T4.host(g).reshape(4, n, d)
+        for lane in range(4):
+            gone = np.zeros(n, bool)
+            gone[bad.get(lane, [])] = True
+            assert np.isnan(g[lane, gone]).all()
+            np.testing.assert_array_equal(g[lane, ~gone], S.bf16(ref[lane, ~gone]))
+    q = torch.randn((2, 4, d), device="cuda").bfloat16()
+    out, lse = eng.kv4_attend(c, eng.counts[0], q)
+    assert out[:, :2].isnan().all() and lse[:, :2].isnan().all()          # lanes 0 and 2
+    assert torch.isfinite(out[:, 2:]).all() and torch.isfinite(lse[:, 2:]).all()
+    # a count out of range leaves its lane
+    before = c.pages.clone()
+    eng.counts[0] = torch.tensor([-1, 101, n, 0], dtype=torch.int32)
+    eng.kv4_pack(0, c)
+    assert eng.last_error()[0] == 9
+    changed = set((c.pages != before).any(1).nonzero().flatten().tolist())
+    assert changed <= set(c.table[2, :5].tolist())
