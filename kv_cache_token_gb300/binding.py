@@ -163,6 +163,13 @@ def kv4_geometry(cfg, device):
     return cfg.batch * cfg.num_kv_heads, lib().kvevict_kv4_page_bytes(ctypes.byref(cfg)), device
 
 
+def _int32(what, *values):
+    # ctypes would pass the low 32 bits on
+    for x in values:
+        if not -0x80000000 <= x <= 0x7FFFFFFF:
+            raise ValueError("%s must be in int32's range, not %d" % (what, x))
+
+
 class Kv4Cache:
     """Device buffers of one 4-bit cache (kvevict_kv4): pages, the lanes' page
     table and the attention's scratch.  Caches of several layers may share one
@@ -432,6 +439,8 @@ class Engine:
         _need(qkv.dim() == 3 and qkv.shape[0] == B and qkv.shape[2] == (Hq + 2 * Hkv) * d and qkv.dtype is dt and
               qkv.get_device() == dev.index and qkv.stride(2) == 1, "qkv must be [batch][n][(Hq + 2 Hkv) d] of the engine's dtype")
         n = qkv.shape[1]
+        r = d if rotary_dim is None else rotary_dim
+        _int32("pos0 and rotary_dim", pos0, r)
         # one token has no next row: its row stride is whatever the tensor says
         row = qkv.stride(1) if n > 1 else (Hq + 2 * Hkv) * d
         for w in (wq, wk):
@@ -445,7 +454,7 @@ class Engine:
         _dense(k, (B, Hkv, n, d), dt, dev, "k")
         _dense(v, (B, Hkv, n, d), dt, dev, "v")
         _check(lib().kvevict_norm_rope(self.h, qkv.data_ptr(), qkv.stride(0), row, n, _raw(wq), _raw(wk), eps,
-                                       _raw(pos), pos0, d if rotary_dim is None else rotary_dim, base,
+                                       _raw(pos), pos0, r, base,
                                        1 if interleaved else 0, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                        self._on(stream)), "kvevict_norm_rope")
         return q, k, v
@@ -455,6 +464,7 @@ class Engine:
         c, dev, bf = self.cfg, self.device, torch.bfloat16
         B, Hq, Hkv, d = c.batch, c.num_q_heads, c.num_kv_heads, c.head_dim
         _need(q.dim() == 4, "q must be [batch][Hq][n][d]")
+        _int32("sinks and window", sinks, window)
         n = q.shape[2]
         _dense(q, (B, Hq, n, d), bf, dev, "q")
         _dense(k, (B, Hkv, n, d), bf, dev, "k")
@@ -498,6 +508,7 @@ class Engine:
 
     def kv4_pack(self, layer, cache, stream=None):
         """kvevict_kv4_pack: every kept token of an engine layer, from index 0."""
+        _int32("layer", layer)
         _check(lib().kvevict_kv4_pack(self.h, layer, self._cache_ref(cache), self._on(stream)), "kvevict_kv4_pack")
 
     def kv4_read(self, cache, starts, n, lens=None, k=None, v=None, stream=None):
@@ -518,6 +529,7 @@ class Engine:
         """kvevict_kv4_attend: (out [B][Hq][d], lse [B][Hq])."""
         c, dev, ref = self.cfg, self.device, self._cache_ref(cache, self.kv4_scratch_bytes)
         shp = (c.batch, c.num_q_heads, c.head_dim)
+        _int32("sinks and window", sinks, window)
         _dense(q, shp, torch.bfloat16, dev, "q")
         if out is None:
             out = self._new(stream, shp, torch.bfloat16)

@@ -154,3 +154,37 @@ def test_default_outputs_belong_to_the_calls_stream(B, monkeypatch, call, output
     assert len(rec.made) == outputs
     assert all(on is s for on, _ in rec.made)
     assert rec.users == ["main"] * outputs              # and kept while the current stream may read them
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 31 - 1, 2 ** 63])
+def test_integers_past_int32_are_refused(B, monkeypatch, big):
+    """ctypes passes the low 32 bits of an integer: a window of 2^32 + 5 would
+    have been 5."""
+    import types
+    e = bare_engine(B)
+    c = bare_cache(B, e)
+    e.device = types.SimpleNamespace(index=-1)
+    seen = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: seen.append(name) or 0
+    monkeypatch.setattr(B, "lib", lambda: Lib())
+    t = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16)
+    x, q, k, lens = t(2, 3, 12 * 128), t(2, 8, 3, 128), t(2, 2, 3, 128), torch.zeros(4, dtype=torch.int32)
+    out, lse = t(2, 3, 8, 128), torch.zeros(2, 8, 3)
+    ro, ao, al, s = dict(q=t(2, 8, 3, 128), k=t(2, 2, 3, 128), v=t(2, 2, 3, 128)), t(2, 8, 128), torch.zeros(2, 8), _Stream()
+    calls = [lambda v: e.norm_rope(x, pos0=v, stream=s, **ro), lambda v: e.norm_rope(x, rotary_dim=v, stream=s, **ro),
+             lambda v: e.attend_prompt(q, k, k, sinks=v, out=out, lse=lse, stream=s),
+             lambda v: e.attend_prompt(q, k, k, window=v, out=out, lse=lse, stream=s),
+             lambda v: e.kv4_attend(c, lens, t(2, 8, 128), sinks=v, out=ao, lse=al, stream=s),
+             lambda v: e.kv4_attend(c, lens, t(2, 8, 128), window=v, out=ao, lse=al, stream=s),
+             lambda v: e.kv4_pack(v, c, stream=s)]
+    for call in calls:
+        with pytest.raises(ValueError, match="int32"):
+            call(big)
+    assert seen == []
+    for call in calls:
+        call(2 ** 31 - 1)
+        call(-2 ** 31)
+    assert len(seen) == 2 * len(calls)      # the library's own checks see these
