@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "kvevict_internal.cuh"
+#include "packed_math.cuh"
 #include "tcgen05.cuh"
 
 namespace kve {
@@ -604,47 +605,8 @@ constexpr uint32_t kIdPV = tc::idesc_bf16(128, kD, 1);
 constexpr uint32_t kId128 = tc::idesc_bf16(128, 128, 0);
 static_assert(kChunkMin % kTileKeys == 0, "chunks hold whole tiles");
 
-// Hardware approximations (PTX ex2/rcp/sqrt .approx.ftz, relative error
-// about 2^-22; results below 2^-126 flush to zero).
-__device__ __forceinline__ float hw_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Two fp32 lanes per instruction (the packed .f32x2 arithmetic): each lane
-// is rounded exactly as the scalar fmaf, + or * rounds it.
-__device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
-      " mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 f2_sub(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n sub.rn.f32x2 d, a, b;\n"
-      " mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 f2_mul(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n"
-      " mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
+// Hardware approximations (PTX rcp/sqrt .approx.ftz, relative error about
+// 2^-22; results below 2^-126 flush to zero).
 __device__ __forceinline__ float hw_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -687,9 +649,6 @@ __device__ __forceinline__ void cp_async4i(int* dst, const int* src) {
 }
 __device__ __forceinline__ void named_arrive(int id, int threads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive1(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // The K and V pool tensor maps of one layer (see kTmapsPerLayer).
@@ -862,7 +821,7 @@ __device__ __forceinline__ void d3_produce(const D3Args& A, const D3Maps& mp, in
       }
     } else {
       __syncwarp();
-      if (lane == 0) mbar_arrive1(&full[st]);   // positions only
+      if (lane == 0) mbar_arrive(&full[st]);   // positions only
     }
     if (kDepth == 0) {
 #pragma unroll
@@ -1036,7 +995,7 @@ __global__ void __launch_bounds__(kP1Threads, 1) d3_p1_kernel(D3Args A, const __
           if (j < j_end) A.ws.d3_vn[lo + j] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive1(&bar.vempty[vs]);
+        if (lane == 0) mbar_arrive(&bar.vempty[vs]);
       }
     }
   } else {
@@ -1056,7 +1015,7 @@ __global__ void __launch_bounds__(kP1Threads, 1) d3_p1_kernel(D3Args A, const __
     cp_wait<0>();
     fence_proxy_async();
     __syncwarp();
-    if (lane == 0) mbar_arrive1(&bar.qfull);
+    if (lane == 0) mbar_arrive(&bar.qfull);
     // pass 2 adds both row tiles' sums into the output: zero it first
     if (nrt > 1 && rt == 0)
       for (int j = j_begin + tid; j < j_end; j += 256) A.col_out[lo + j] = 0.f;
@@ -1103,7 +1062,7 @@ __global__ void __launch_bounds__(kP1Threads, 1) d3_p1_kernel(D3Args A, const __
       // the stage is free once S(t) is done (x_full) and the rows are past
       // its positions
       __syncwarp();
-      if (lane == 0) mbar_arrive1(&bar.kempty[ks]);
+      if (lane == 0) mbar_arrive(&bar.kempty[ks]);
       // The row loops stay compact (16 keys at a time, S read twice: max,
       // then P): the kernel's warp roles share the instruction cache, and
       // fully unrolled loops stalled them on instruction fetch.  Without P V
@@ -1202,7 +1161,7 @@ __global__ void __launch_bounds__(kP1Threads, 1) d3_p1_kernel(D3Args A, const __
         // S is read: release the buffer
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive1(&bar.x_free[b]);
+        if (lane == 0) mbar_arrive(&bar.x_free[b]);
         continue;
       }
       // p = 2^(s scale2 - m); a key the row does not see gives 0, and so does
@@ -1293,7 +1252,7 @@ __global__ void __launch_bounds__(kP1Threads, 1) d3_p1_kernel(D3Args A, const __
       tc::wait_st();
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive1(&bar.x_free[b]);
+      if (lane == 0) mbar_arrive(&bar.x_free[b]);
     }
     // merge the two key halves' (max, sum, O) per row, like two chunks;
     // this thread writes output columns [64 h, 64 h + 64)
@@ -1475,7 +1434,7 @@ __global__ void __launch_bounds__(kP2Threads, 1) d3_p2_kernel(D3Args A, const __
     cp_wait<0>();
     fence_proxy_async();
     named_sync(1, kRowThreads);
-    if (lane == 0) mbar_arrive1(&sm.qfull);
+    if (lane == 0) mbar_arrive(&sm.qfull);
     // the query position of row r0 + lane, and the warp's minimum: a key at
     // or before it is seen by all of the warp's rows
     const int qp_mine = r0 + lane < A.rows ? A.qpos[(r0 + lane) % A.w] : 0x7FFFFFFF;
@@ -1631,7 +1590,7 @@ __global__ void __launch_bounds__(kP2Threads, 1) d3_p2_kernel(D3Args A, const __
         tc::fence_before();
         named_arrive(hb, 128);
         __syncwarp();
-        if (lane == 0) mbar_arrive1(&sm.x_free[st]);
+        if (lane == 0) mbar_arrive(&sm.x_free[st]);
       } else {
         named_sync(hb, 128);
         tc::fence_after();
@@ -1640,7 +1599,7 @@ __global__ void __launch_bounds__(kP2Threads, 1) d3_p2_kernel(D3Args A, const __
         const float tot = ((acc + __uint_as_float(a1)) + __uint_as_float(a2)) + __uint_as_float(a3);
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive1(&sm.x_free[st]);
+        if (lane == 0) mbar_arrive(&sm.x_free[st]);
         if (key_ok) {
           if (nrt == 1)
             A.col_out[lo + j] = tot;

@@ -22,6 +22,7 @@
 // shared memory) that fits on an SM beside three CTAs of the attention
 // kernel, so the epilogue of one layer runs while the next layer streams.
 #include "lane_ops.cuh"
+#include "packed_math.cuh"
 
 #include <cooperative_groups.h>
 
@@ -76,14 +77,6 @@ __device__ __forceinline__ void lane_step(const EpiArgs& A, const LaneRefs& L, c
                                           unsigned char* dsm, int* sh_work, int* sh_gen);
 __device__ void allocate_layer(const LayerState& ls, const Workspace& ws, const Dims& dm, int* sh_scan,
                                int* sh_flag);
-
-// 2^x by the hardware approximation (PTX ex2.approx.ftz, relative error
-// about 2^-22; results below 2^-126 flush to zero).
-__device__ __forceinline__ float hw_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // DropKV decode variant: this step's residual-output score of every kept
 // token, written to column rs of its history-ring row: the sum over the

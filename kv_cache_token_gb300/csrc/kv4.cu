@@ -13,6 +13,7 @@
 // TB/s.  Reading back is bound by memory: the same tokens in 32 us, 5.4 TB/s.
 #include "kv4_page.cuh"
 #include "kvevict_internal.cuh"
+#include "packed_math.cuh"
 
 namespace kve {
 
@@ -46,31 +47,6 @@ __device__ __forceinline__ float div_rn(float x, float scale, float rcp) {
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
 __device__ __forceinline__ __nv_bfloat162 max_abs(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmax2_nan(a, b); }
-// two fp32 numbers an instruction, each rounded as the scalar one
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n"
-      " mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
-      " mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 
 // grid (groups of `per` pages a lane can touch, lanes).  The rows of the next
 // page are loaded while one is coded.
@@ -201,8 +177,8 @@ __global__ void __launch_bounds__(kKv4Threads, 5) kv4_store_kernel(Kv4Store a, i
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 x = make_float2(__uint_as_float(uw[j] << 16), __uint_as_float(uw[j] & 0xFFFF0000u));
-          const float2 q = mul2(x, rc);
-          const float2 y = add2(fma2(fma2(q, ns, x), rc, q), magic);
+          const float2 q = f2_mul(x, rc);
+          const float2 y = f2_add(f2_fma(f2_fma(q, ns, x), rc, q), magic);
           code[2 * j] = __float_as_uint(y.x);
           code[2 * j + 1] = __float_as_uint(y.y);
         }

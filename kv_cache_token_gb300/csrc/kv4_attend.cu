@@ -43,6 +43,7 @@
 // warps with two pages (spilled registers) 74.
 #include "kv4_page.cuh"
 #include "kvevict_internal.cuh"
+#include "packed_math.cuh"
 
 namespace kve {
 
@@ -143,15 +144,6 @@ __device__ __forceinline__ void code_pairs(uint32_t word, uint32_t (&x)[4]) {
   x[1] = word & 0x03C003C0u;
   x[2] = r & 0x003C003Cu;
   x[3] = r & 0x03C003C0u;
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-// 2^x; results below 2^-126 are zero
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
@@ -452,7 +444,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kThreads, 1) kv4_attend_kernel(
       for (int w = 0; w < W; ++w) {
         const float mw = sh_ml[w][h][0];
         // a warp without a page has zero sums; one of NaN alone has no maximum
-        const float f = mw == -INFINITY ? 1.f : ex2(mw - M);
+        const float f = mw == -INFINITY ? 1.f : hw_exp2(mw - M);
         const float4 v = *reinterpret_cast<const float4*>(sh_o + (w * C::kHeads + h) * C::kOStride + 4 * d4);
         L = fmaf(sh_ml[w][h][1], f, L);
         acc.x = fmaf(v.x, f, acc.x);
@@ -629,7 +621,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kThreads, 1) kv4_attend_kernel(
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
           const float mo = m_run[nt][e], mn = fmaxf(mo, t);
-          const float c = mo == -INFINITY ? 0.f : ex2(mo - mn);
+          const float c = mo == -INFINITY ? 0.f : hw_exp2(mo - mn);
           m_run[nt][e] = mn;
           l_run[nt][e] *= c;
 #pragma unroll
@@ -646,7 +638,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kThreads, 1) kv4_attend_kernel(
       for (int p = 0; p < NP; ++p) {
         float u[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = ex2(z[p][nt][e] - (e & 1 ? m1 : m0));
+        for (int e = 0; e < 4; ++e) u[e] = hw_exp2(z[p][nt][e] - (e & 1 ? m1 : m0));
         l_run[nt][0] = fmaf(u[0], g0[p], fmaf(u[2], g1[p], l_run[nt][0]));
         l_run[nt][1] = fmaf(u[1], g0[p], fmaf(u[3], g1[p], l_run[nt][1]));
         bt[p][nt][0] = transpose8x8(half2_bits(u[0], u[1]));
@@ -734,7 +726,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kThreads, 1) kv4_attend_kernel(
       M = warp_max(M);
       for (int c = c0 + lane_id; c <= c1; c += 32) {
         const float4 x = __ldcg(reinterpret_cast<const float4*>(part_of(c, c > c0 || first_at_start) + h * (D + 4) + D));
-        const float f = x.x == -INFINITY ? 1.f : ex2(x.x - M);
+        const float f = x.x == -INFINITY ? 1.f : hw_exp2(x.x - M);
         sh_o[(c - c0) * C::kHeads + h] = f;
         L = fmaf(x.y, f, L);
       }

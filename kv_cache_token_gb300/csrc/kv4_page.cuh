@@ -45,8 +45,6 @@ struct Kv4Page {
   }
   __device__ static __forceinline__ uint32_t pack(uint32_t nibbles) { return __funnelshift_l(nibbles, nibbles, 2); }
   __device__ static __forceinline__ uint32_t unpack(uint32_t word) { return __funnelshift_r(word, word, 2); }
-  // nibble of token t within its V word, row half hi (elements + 8)
-  __host__ __device__ static constexpr int v_nibble(int t, int hi) { return hi + (t >= 8 ? 2 : 0) + (t & 1) * 4; }
   __host__ __device__ static constexpr int v_ratio(int t, int w) {
     return (((t & 7) >> 1) * kG + w) * 4 + (t & 1) + (t >= 8 ? 2 : 0);
   }

@@ -22,6 +22,7 @@
 #include <cstring>
 
 #include "kvevict_internal.cuh"
+#include "packed_math.cuh"
 #include "rope_turns.h"
 
 namespace kve {
@@ -42,23 +43,6 @@ struct RopeArgs {
   int tok;             // tokens of a CTA
   uint64_t freq[kRopePairs];   // fractions of a turn per position
 };
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n"
-      " mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 
 // Four elements: 8 bytes of bf16, 16 of fp32.
 template <typename T>
@@ -177,20 +161,20 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
           Q::unpack(xa[j], x);
           Q::unpack(xb[j], x + 2);
           if (w[j]) {
-            float2 sq = mul2(x[0], x[0]);
-            sq = fma2(x[1], x[1], sq);
-            sq = fma2(x[2], x[2], sq);
-            sq = fma2(x[3], x[3], sq);
+            float2 sq = f2_mul(x[0], x[0]);
+            sq = f2_fma(x[1], x[1], sq);
+            sq = f2_fma(x[2], x[2], sq);
+            sq = f2_fma(x[3], x[3], sq);
             float ss = sq.x + sq.y;
 #pragma unroll
             for (int m = kRow / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(who, ss, m);
             const float inv = rsqrtf(ss * (1.f / D) + a.eps);
             const float4 wa = reinterpret_cast<const float4*>(w[j])[qa], wb = reinterpret_cast<const float4*>(w[j])[qb];
             const float2 iv = make_float2(inv, inv);
-            x[0] = mul2(mul2(x[0], iv), make_float2(wa.x, wa.y));
-            x[1] = mul2(mul2(x[1], iv), make_float2(wa.z, wa.w));
-            x[2] = mul2(mul2(x[2], iv), make_float2(wb.x, wb.y));
-            x[3] = mul2(mul2(x[3], iv), make_float2(wb.z, wb.w));
+            x[0] = f2_mul(f2_mul(x[0], iv), make_float2(wa.x, wa.y));
+            x[1] = f2_mul(f2_mul(x[1], iv), make_float2(wa.z, wa.w));
+            x[2] = f2_mul(f2_mul(x[2], iv), make_float2(wb.x, wb.y));
+            x[3] = f2_mul(f2_mul(x[3], iv), make_float2(wb.z, wb.w));
           }
           if (turns) {
             if (kInterleaved) {
@@ -198,13 +182,13 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
               for (int i = 0; i < 4; ++i) {
                 const float cc = i == 0 ? c0.x : i == 1 ? c0.y : i == 2 ? c1.x : c1.y;
                 const float ss = i == 0 ? s0.x : i == 1 ? s0.y : i == 2 ? s1.x : s1.y;
-                x[i] = fma2(x[i], make_float2(cc, cc), mul2(make_float2(x[i].y, x[i].x), make_float2(-ss, ss)));
+                x[i] = f2_fma(x[i], make_float2(cc, cc), f2_mul(make_float2(x[i].y, x[i].x), make_float2(-ss, ss)));
               }
             } else {
               const float2 n0 = make_float2(-s0.x, -s0.y), n1 = make_float2(-s1.x, -s1.y);
-              const float2 y0 = fma2(x[0], c0, mul2(x[2], n0)), y1 = fma2(x[1], c1, mul2(x[3], n1));
-              x[2] = fma2(x[2], c0, mul2(x[0], s0));
-              x[3] = fma2(x[3], c1, mul2(x[1], s1));
+              const float2 y0 = f2_fma(x[0], c0, f2_mul(x[2], n0)), y1 = f2_fma(x[1], c1, f2_mul(x[3], n1));
+              x[2] = f2_fma(x[2], c0, f2_mul(x[0], s0));
+              x[3] = f2_fma(x[3], c1, f2_mul(x[1], s1));
               x[0] = y0;
               x[1] = y1;
             }

@@ -44,6 +44,7 @@
 #include <cudaTypedefs.h>
 
 #include "kvevict_internal.cuh"
+#include "packed_math.cuh"
 #include "tcgen05.cuh"
 
 namespace kve {
@@ -95,28 +96,6 @@ struct RowTile {
   }
 };
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
-      " mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-// 2^x; results below 2^-126 are zero
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -143,9 +122,6 @@ __device__ __forceinline__ void mbar_sleep(uint64_t* bar, uint32_t parity, uint3
     if (ok) return;
   }
   set_status(status, ST_TIMEOUT);
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
@@ -408,7 +384,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const PromptA
       const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
       float factor = 1.f;
       if (tmax > m_run + kPromptGrow) {
-        factor = m_run == -INFINITY ? 0.f : ex2(m_run - tmax);
+        factor = m_run == -INFINITY ? 0.f : hw_exp2(m_run - tmax);
         m_run = tmax;
         l_run *= factor;
       }
@@ -426,9 +402,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const PromptA
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             uint32_t* v = &s[c][2 * e];
-            const float2 y = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), sc, nm);
-            v[0] = __float_as_uint(ex2(y.x));
-            v[1] = __float_as_uint(ex2(y.y));
+            const float2 y = f2_fma(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), sc, nm);
+            v[0] = __float_as_uint(hw_exp2(y.x));
+            v[1] = __float_as_uint(hw_exp2(y.y));
           }
         }
         if (c > 0) {
@@ -437,8 +413,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const PromptA
           for (int e = 0; e < 8; ++e) {
             const uint32_t* v = &s[c - 1][2 * e];
             const float2 z = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
-            if (e & 1) sum1 = add2(sum1, z);
-            else sum0 = add2(sum0, z);
+            if (e & 1) sum1 = f2_add(sum1, z);
+            else sum0 = f2_add(sum0, z);
             p[e] = bf16x2(z.x, z.y);
           }
           tc::st8(aS + (c - 1) * 8, p);
