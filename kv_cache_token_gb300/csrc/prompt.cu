@@ -109,8 +109,12 @@ __device__ __forceinline__ bool elect_one() {
 }
 // mbar_wait_bounded with a long suspension a poll (100 us; a completed phase ends
 // it at once): a waiting warp that polls often takes issue slots from the other
-// row tile's exponentials.  Gives up after 2^14 polls, about a second and a half.
-__device__ __forceinline__ void mbar_sleep(uint64_t* bar, uint32_t parity, uint32_t* status) {
+// row tile's exponentials.  Gives up after 2^14 polls, about a second and a half,
+// and returns false.  A prompt has hundreds of waits a CTA, each behind the one
+// that failed, so the caller then waits no more: copies and MMAs end, and the
+// softmax, whose warps must stay together, runs on without waiting.  Nothing is
+// in flight by then: whoever gives up, the others have waited about as long.
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity, uint32_t* status) {
   const uint32_t at = smem_u32(bar);
   for (int i = 0; i < (1 << 14); ++i) {
     uint32_t ok;
@@ -119,9 +123,10 @@ __device__ __forceinline__ void mbar_sleep(uint64_t* bar, uint32_t parity, uint3
         : "=r"(ok)
         : "r"(at), "r"(parity), "r"(100000)
         : "memory");
-    if (ok) return;
+    if (__builtin_expect(ok, 1)) return true;
   }
   set_status(status, ST_TIMEOUT);
+  return false;
 }
 __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
@@ -234,73 +239,75 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const PromptA
       }
       for (int u = 0; u < 2 * tiles; ++u) {
         const int s = u % C::kSlots, use = u / C::kSlots;
-        if (use > 0) mbar_sleep(&bar.empty[s], (use - 1) & 1, a.status);
+        if (use > 0 && !mbar_sleep(&bar.empty[s], (use - 1) & 1, a.status)) break;
         mbar_arrive_expect_tx(&bar.full[s], C::kTile);
         const CUtensorMap* m = (u & 1) ? &mp.v : &mp.k;
         for (int c = 0; c < C::kHalves; ++c)
           tma_load3(skv + s * C::kTile + c * (kKeyTile * 128), m, c * 64, tile_of(u >> 1) * kKeyTile, lane, &bar.full[s]);
       }
     } else if (warp == kMmaWarp) {
-      // The whole warp runs the loop (so that descriptors stay in uniform
-      // registers) and one thread issues.  Everything a step needs is ready
-      // before its waits: bookkeeping between a wait and an issue is time the
-      // tensor cores idle.
-      const uint32_t leader = elect_one() ? 1u : 0u;
-      const uint64_t dq0 = tc::desc_sw128(smem_u32(sq), 16, 1024);
-      const uint64_t dk0 = tc::desc_sw128(smem_u32(skv), 16, 1024);
-      const uint64_t dv0 = tc::desc_sw128(smem_u32(skv), kKeyTile * 128, 1024);
-      mbar_sleep(&bar.q_full, 0, a.status);
-      uint32_t done[2] = {0u, 0u};                 // P V products of a row tile so far
-      bool now[2], before[2] = {false, false};
-      int sk = 0, kphase = 0, sv = 1, vphase = 0;  // ring slots of K(t) and V(t - 1), and their phases
+      [&] {
+        // The whole warp runs the loop (so that descriptors stay in uniform
+        // registers) and one thread issues.  Everything a step needs is ready
+        // before its waits: bookkeeping between a wait and an issue is time the
+        // tensor cores idle.
+        const uint32_t leader = elect_one() ? 1u : 0u;
+        const uint64_t dq0 = tc::desc_sw128(smem_u32(sq), 16, 1024);
+        const uint64_t dk0 = tc::desc_sw128(smem_u32(skv), 16, 1024);
+        const uint64_t dv0 = tc::desc_sw128(smem_u32(skv), kKeyTile * 128, 1024);
+        if (!mbar_sleep(&bar.q_full, 0, a.status)) return;
+        uint32_t done[2] = {0u, 0u};                 // P V products of a row tile so far
+        bool now[2], before[2] = {false, false};
+        int sk = 0, kphase = 0, sv = 1, vphase = 0;  // ring slots of K(t) and V(t - 1), and their phases
 #pragma unroll
-      for (int h = 0; h < 2; ++h) now[h] = rt[h].active(0, sink_tiles);
-      // step t: O += P V(t - 1), then S(t), a row tile at a time
+        for (int h = 0; h < 2; ++h) now[h] = rt[h].active(0, sink_tiles);
+        // step t: O += P V(t - 1), then S(t), a row tile at a time
 #pragma unroll 1
-      for (int t = 0; t <= tiles; ++t) {
-        const uint64_t dv = tc::desc_add(dv0, sv * C::kTile), dk = tc::desc_add(dk0, sk * C::kTile);
-        if (t > 0) mbar_sleep(&bar.full[sv], vphase, a.status);
-        bool k_there = false;
+        for (int t = 0; t <= tiles; ++t) {
+          const uint64_t dv = tc::desc_add(dv0, sv * C::kTile), dk = tc::desc_add(dk0, sk * C::kTile);
+          if (t > 0 && !mbar_sleep(&bar.full[sv], vphase, a.status)) return;
+          bool k_there = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (before[h]) {
-            const uint32_t acc = done[h] > 0 ? 1u : 0u;
-            mbar_sleep(&bar.p_full[h], done[h] & 1u, a.status);
-            tc::fence_after();
+          for (int h = 0; h < 2; ++h) {
+            if (before[h]) {
+              const uint32_t acc = done[h] > 0 ? 1u : 0u;
+              if (!mbar_sleep(&bar.p_full[h], done[h] & 1u, a.status)) return;
+              tc::fence_after();
 #pragma unroll
-            for (int ks = 0; ks < kKeyTile / 16; ++ks)
-              mma_ts_if(leader, tm + C::kOCol + h * 128, tm + h * 128 + ks * 8, tc::desc_add(dv, ks * 2048), C::kIdO,
-                        ks > 0 ? 1u : acc);
-            if (t - 1 == rt[h].to) commit_if(leader, &bar.o_full[h]);
-            ++done[h];
-          }
-          if (now[h]) {
-            if (!k_there) mbar_sleep(&bar.full[sk], kphase, a.status);
-            k_there = true;
-            tc::fence_after();
-            const uint64_t dq = tc::desc_add(dq0, h * C::kTile);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const int off = (ks >> 2) * (kKeyTile * 128) + (ks & 3) * 32;
-              mma_ss_if(leader, tm + h * 128, tc::desc_add(dq, off), tc::desc_add(dk, off), C::kIdS, ks > 0 ? 1u : 0u);
+              for (int ks = 0; ks < kKeyTile / 16; ++ks)
+                mma_ts_if(leader, tm + C::kOCol + h * 128, tm + h * 128 + ks * 8, tc::desc_add(dv, ks * 2048), C::kIdO,
+                          ks > 0 ? 1u : acc);
+              if (t - 1 == rt[h].to) commit_if(leader, &bar.o_full[h]);
+              ++done[h];
             }
-            commit_if(leader, &bar.s_full[h]);
+            if (now[h]) {
+              if (!k_there && !mbar_sleep(&bar.full[sk], kphase, a.status)) return;
+              k_there = true;
+              tc::fence_after();
+              const uint64_t dq = tc::desc_add(dq0, h * C::kTile);
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const int off = (ks >> 2) * (kKeyTile * 128) + (ks & 3) * 32;
+                mma_ss_if(leader, tm + h * 128, tc::desc_add(dq, off), tc::desc_add(dk, off), C::kIdS, ks > 0 ? 1u : 0u);
+              }
+              commit_if(leader, &bar.s_full[h]);
+            }
+          }
+          if (t < tiles) commit_if(leader, &bar.empty[sk]);
+          if (t > 0) commit_if(leader, &bar.empty[sv]);
+          sk += 2;
+          if (sk >= C::kSlots) { sk -= C::kSlots; kphase ^= 1; }
+          if (t > 0) {
+            sv += 2;
+            if (sv >= C::kSlots) { sv -= C::kSlots; vphase ^= 1; }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            before[h] = now[h];
+            now[h] = t + 1 < tiles && rt[h].active(t + 1, sink_tiles);
           }
         }
-        if (t < tiles) commit_if(leader, &bar.empty[sk]);
-        if (t > 0) commit_if(leader, &bar.empty[sv]);
-        sk += 2;
-        if (sk >= C::kSlots) { sk -= C::kSlots; kphase ^= 1; }
-        if (t > 0) {
-          sv += 2;
-          if (sv >= C::kSlots) { sv -= C::kSlots; vphase ^= 1; }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          before[h] = now[h];
-          now[h] = t + 1 < tiles && rt[h].active(t + 1, sink_tiles);
-        }
-      }
+      }();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -314,13 +321,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const PromptA
     const float2 sc = make_float2(a.scale2, a.scale2);
     float m_run = -INFINITY, l_run = 0.f;
     int cnt = 0;
+    bool alive = true;         // no wait has given up
 #pragma unroll 1
     for (int t = 0; t < tiles; ++t) {
       const int tile = tile_of(t);
       if (!my.active(t, sink_tiles)) continue;
       const bool full = my.full(tile, a.sinks, a.window);
       const int k0 = tile * kKeyTile;
-      mbar_sleep(&bar.s_full[h], cnt & 1, a.status);
+      if (alive) alive = mbar_sleep(&bar.s_full[h], cnt & 1, a.status);
       tc::fence_after();
       uint32_t s[8][16];
 #pragma unroll
@@ -347,7 +355,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const PromptA
         const int key = k0 + row;
         if (!(key <= my.a && (key >= my.b - a.window + 1 || key < a.sinks))) {
           const int u = 2 * t + 1, sl = u % C::kSlots;
-          mbar_sleep(&bar.full[sl], (u / C::kSlots) & 1, a.status);
+          if (alive) alive = mbar_sleep(&bar.full[sl], (u / C::kSlots) & 1, a.status);
           unsigned char* vr = skv + sl * C::kTile + row * 128;
           bool bad = false;
 #pragma unroll 1
@@ -442,7 +450,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const PromptA
       ++cnt;
     }
     if (cnt > 0) {
-      mbar_sleep(&bar.o_full[h], 0, a.status);
+      if (alive) (void)mbar_sleep(&bar.o_full[h], 0, a.status);
       tc::fence_after();
     }
     // the other row tile may have zeroed values this one's rows see
