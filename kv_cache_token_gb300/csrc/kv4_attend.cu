@@ -319,6 +319,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kThreads, 1) kv4_attend_kernel(
         __syncwarp();
       }
     }
+    // (a consumer that gave up waiting runs ahead of its copies: the CTA ends after they have landed)
+    for (int i = max(0, sent - S); i < sent; ++i) (void)mbar_wait_bounded(&sh_full[mine][i % S], (i / S) & 1, a.status);
     return;
   }
 
