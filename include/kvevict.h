@@ -388,8 +388,8 @@ kvevict_status kvevict_attend_static(kvevict_ctx* ctx, int layer, const void* q,
  * the q, k_new, v_new of kvevict_decode_step, else the q of
  * kvevict_attend_prompt and the k_ctx, v_ctx of kvevict_prefill.
  * Token t of every sequence is at pos[t] (int32 [n], device), or at pos0 + t
- * when pos is NULL.  Angles are within 2^-25 of a turn at every int32 position
- * for bases from 1 (2^-26 is their fp32 rounding); below, what the frequencies
+ * when pos is NULL.  Angles are within 2^-27 of a turn at every int32 position
+ * for bases from 1 (2^-28 is their fp32 rounding); below, what the frequencies
  * are off by, |p| * 2^-61 of a turn at most, grows by 1 / base.
  * KVEVICT_E_INVALID_ARG: n < 1; qkv or an output NULL; qkv, outputs or weights
  * not 16-byte aligned; strides not a multiple of 16 bytes, row_stride <
