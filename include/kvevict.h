@@ -383,7 +383,8 @@ kvevict_status kvevict_attend_static(kvevict_ctx* ctx, int layer, const void* q,
  *   pair i being elements (i, i + rotary_dim/2), or (2i, 2i + 1) when
  *   `interleaved` is not 0; the others pass.
  * Value heads are copied.  Results are computed in fp32 and rounded once (a
- * head whose sum of squares passes fp32's range has a norm of infinity).
+ * head whose sum of squares passes fp32's range has a norm of infinity; one
+ * whose squares all fall below it, of sqrt(eps)).
  * q_out [B][Hq][n][d], k_out and v_out [B][Hkv][n][d] (kv_dtype): with n = 1
  * the q, k_new, v_new of kvevict_decode_step, else the q of
  * kvevict_attend_prompt and the k_ctx, v_ctx of kvevict_prefill.
@@ -488,9 +489,17 @@ kvevict_status kvevict_kv4_read(kvevict_ctx* ctx, const kvevict_kv4* cache, cons
  * device) of each lane attend its first lens[lane] tokens (int32 [B*Hkv],
  * device), or, with window > 0, the first `sinks` and the last `window` of
  * them.  Writes out [B][Hq][d] (bf16) and, unless NULL, lse [B][Hq] (fp32,
- * natural log).  A lane without tokens gets zeros and -inf.  lens below 0 or
- * past the table is clamped and reported (index out of range), as is a page
- * id out of range (page 0 is read in its place). */
+ * natural log).  A lane without tokens gets zeros and -inf.  Sums, maxima and
+ * the output accumulate in fp32; the products' operands are fp16:
+ *   a head's query, scaled by a power of two: elements below 2^-26 of the
+ *   head's largest lose bits;
+ *   the codes, as subnormals: a product's sum over 16 elements is cut at 2^-15
+ *   of a code's unit (its scale) times their largest |q|;
+ *   a weight, and its product with the value scale, 11 bits each: below 2^-33
+ *   of the head's largest such product it is lost from out, not from lse.
+ * Scaled logits must stay within fp32's range.  lens below 0 or past the table
+ * is clamped and reported (index out of range), as is a page id out of range
+ * (page 0 is read in its place). */
 kvevict_status kvevict_kv4_attend(kvevict_ctx* ctx, const kvevict_kv4* cache, const int32_t* lens,
                                   const void* q, int32_t sinks, int32_t window, void* out, float* lse,
                                   void* stream);

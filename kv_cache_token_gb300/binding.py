@@ -175,7 +175,8 @@ class Kv4Cache:
     table and the attention's scratch.  Caches of several layers may share one
     pool of pages: pass `pages`, and a table per layer.  Other engines of the
     same lanes, head_dim and device may use the cache (to attend, no larger
-    a group); any other engine's calls refuse it."""
+    a group); any other engine's calls refuse it.  Pages and scratch start at
+    zero on the stream that is current here: another stream waits for it."""
 
     def __init__(self, eng, num_pages, max_pages, table=None, pages=None):
         L, c = lib(), ctypes.byref(eng.cfg)

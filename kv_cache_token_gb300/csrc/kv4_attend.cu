@@ -36,11 +36,12 @@
 //
 // Measured: 16 lanes of 131072 tokens, groups of 4 (304 MB): 69 us, 4.4 TB/s,
 // 0.65 of the measured copy bandwidth (the copies alone, without the work on
-// them, 56 us); 128 lanes of 3276 tokens, groups of 8: 19.3 us, of which the
-// stream is 13.  Bound by issue: 285 instructions a page, 0.43 of the slots,
-// with the data path not far behind (12 warps a SM are all that the
-// accumulators leave room for).  One page a tile with 15 warps took 78 us, 15
-// warps with two pages (spilled registers) 74.
+// them, 56 us); 128 lanes of 3276 tokens, groups of 8: 19.8 us, of which the
+// stream is 13.  Bound by latency: 289 instructions a page take 0.43 of the issue
+// slots and as much of the integer pipe, but a scheduler has three warps (12 a SM
+// are all that the accumulators leave room for), each a chain of masks, MMAs and
+// exponentials, and a round's copies wait for its slowest warp.  One page a tile
+// with 15 warps took 78 us, 15 warps with two pages (spilled registers) 74.
 #include "kv4_page.cuh"
 #include "kvevict_internal.cuh"
 #include "packed_math.cuh"
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kThreads, 1) kv4_attend_kernel(
   __syncthreads();
   // Equal runs of rounds, or, with a CTA for every lane, a lane each where the
   // longest lane is no longer than a run and the join it spares (128 lanes of
-  // 3276 tokens: 19.3 us, against 26.2 in equal runs; 32 lanes of 516: 8.0
+  // 3276 tokens: 19.8 us, against 26.2 in equal runs; 32 lanes of 516: 8.0
   // against 10.6).
   const long long R = sh_prefix[a.lanes], G = min(static_cast<long long>(gridDim.x), R);   // G runs, none empty
   const bool lane_each = a.lanes <= gridDim.x && sh_most <= (R + gridDim.x - 1) / gridDim.x + kJoinRounds;

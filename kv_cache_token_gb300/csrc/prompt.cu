@@ -24,22 +24,26 @@
 // shared memory first, noted, and added at the end to the rows that do see
 // them.
 //
-// Measured (d = 128): 16384 tokens, 32 heads, every earlier key: 1.47 ms, 1500
-// TFLOP/s, 0.79 of the measured bf16 burst rate (0.86 of the sustained one);
-// 16385 tokens, 64 heads, window 4096 and 4 sinks: 1.58 ms, 1220 TFLOP/s, the
-// rest in the three masked tiles of every 35 and in starting 4104 CTAs.  Bound
-// by the chain of one row tile, S to P to P V and the next S (tensor memory
-// holds no second S beside two O of 128 columns): of 3150 cycles a tile the
-// softmax takes 1400, its own MMAs 1024, and the other row tile's MMAs and four
-// hand-overs the rest; the tensor pipe is active 59% of the time.  Halving the
-// bytes of K and V per tile gains 3%.  Slower were: P handed over in halves (the
+// Measured (d = 128), ten launches in a row at 2070 MHz and several hundred, where
+// the power limit holds the clock near 1930: 16384 tokens, 32 heads, every
+// earlier key 1.42 / 1.52 ms, 1550 / 1450 TFLOP/s, 0.78 / 0.83 of the measured
+// bf16 rate of a burst / of seconds; 16385 tokens, 64 heads, window 4096 and 4
+// sinks 1.57 / 1.62 ms, 1220 / 1190 TFLOP/s, the rest in the three masked tiles of
+// every 35 and in starting 4104 CTAs.  No unit is full (8192 tokens: tensor pipe
+// active 59% of the time, issue slots 38%): a row tile's chain, S to P to P V and
+// the next S, is what a tile takes (tensor memory holds no second S beside two O
+// of 128 columns): of 3150 cycles the softmax takes 1400, its own MMAs 1024, and
+// the other row tile's MMAs and four hand-overs the rest.  Halving the bytes of K
+// and V per tile gains 3%.  Slower were, at d = 128: P handed over in halves (the
 // in-order issuer then waits for one row tile with the other ready), an issuing
 // warp a row tile (both chains then run in step and share the tensor cores; 7%
 // with P in halves, 14% without), the maximum taken alongside the exponentials,
 // two threads a row, key tiles of 64 with two S buffers, and part of the
-// exponentials by a polynomial.  Heads of 64 take 1.17 ms for the 16384 tokens
-// (S of the next tile computed beside P, which they have room for, changes
-// nothing: the softmax bounds them).
+// exponentials by a polynomial.  Heads of 64 take 1.14 ms for the 16384 tokens,
+// 970 TFLOP/s.  There too no unit is full (8192 tokens: issue slots 45%,
+// exponentials 38%, tensor pipe 37%): two softmax warps a scheduler, each a chain
+// of dependent steps.  S of the next tile computed beside P, which d = 64 has room
+// for, changed nothing; two threads a row were not tried there.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
