@@ -162,3 +162,39 @@ def test_host_threads_with_bases_of_their_own():
         th.join()
     assert codes == [0] * 4 and wrong == [0] * 4, (codes, wrong)
     assert eng.last_error()[0] == 0
+
+
+def test_captured_calls_on_a_forked_stream():
+    """A captured graph whose calls run on a forked stream and make their own
+    outputs: replays follow the inputs."""
+    eng = Engine(config_from(policy=H2O, num_layers=1, batch=2, num_q_heads=8, num_kv_heads=2, head_dim=128, kv_dtype=BF16,
+                             blocks_per_pool=4, max_tokens=8, budget=4, recent_window=2, obs_window=1, pool_kernel=1))
+    eng.reset()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    c = eng.kv4_cache(4 * 5, 5)
+    x, lens = rnd(2, 1, 12 * 128), torch.full((4,), 70, dtype=torch.int32, device="cuda")
+    eng.kv4_write(c, None, rnd(2, 2, 80, 128), rnd(2, 2, 80, 128))
+
+    def step(stream=None):
+        q, k, v = eng.norm_rope(x, pos0=70, stream=stream)
+        eng.kv4_write(c, lens, k, v, stream=stream)
+        out = eng.kv4_attend(c, lens, q.view(2, 8, 128), sinks=2, window=40, stream=stream)
+        return [q, k, v, *out, *eng.kv4_read(c, lens, 4, stream=stream)]
+
+    step()
+    side, cap = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=cap):
+        side.wait_stream(cap)
+        outs = step(side)
+        cap.wait_stream(side)
+    for _ in range(3):
+        x.copy_(rnd(2, 1, 12 * 128))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        ref = step()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert eng.last_error()[0] == 0
