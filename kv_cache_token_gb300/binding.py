@@ -163,11 +163,10 @@ def kv4_geometry(cfg, device):
     return cfg.batch * cfg.num_kv_heads, lib().kvevict_kv4_page_bytes(ctypes.byref(cfg)), device
 
 
-def _int32(what, *values):
+def _int32(what, a, b=0):
     # ctypes would pass the low 32 bits on
-    for x in values:
-        if not -0x80000000 <= x <= 0x7FFFFFFF:
-            raise ValueError("%s must be in int32's range, not %d" % (what, x))
+    if not (-0x80000000 <= a <= 0x7FFFFFFF and -0x80000000 <= b <= 0x7FFFFFFF):
+        raise ValueError("%s must be in int32's range, not %d, %d" % (what, a, b))
 
 
 class Kv4Cache:
@@ -180,7 +179,7 @@ class Kv4Cache:
 
     def __init__(self, eng, num_pages, max_pages, table=None, pages=None):
         L, c = lib(), ctypes.byref(eng.cfg)
-        self.geometry = kv4_geometry(eng.cfg, eng.device)
+        self.geometry = eng.kv4_geometry
         page = self.geometry[1]
         if page == 0:
             raise KvevictError(6, "kvevict_kv4_page_bytes")
@@ -487,7 +486,7 @@ class Engine:
 
     def _cache_ref(self, cache, scratch=0):
         # the library sees addresses only: a cache sized for other lanes or rows would be overrun
-        if not (cache.geometry == self.kv4_geometry and cache.scratch_bytes >= scratch):
+        if not ((cache.geometry is self.kv4_geometry or cache.geometry == self.kv4_geometry) and cache.scratch_bytes >= scratch):
             raise ValueError("the cache was made for %s (lanes, page bytes, device) and %d bytes of scratch; this engine needs %s and %d"
                              % (cache.geometry, cache.scratch_bytes, self.kv4_geometry, scratch))
         return cache.ref
